@@ -73,8 +73,9 @@ typedef enum {
 
 /* MLA_FP8_CACHE: activations, weights and output bf16; the cache holds per
  * token r E4M3 codes of cKV, one fp32 scale s_t and the RoPE key in bf16
- * divided by s_t (see mla_decode_run_fp8). Tensor-core path, one latent shard. */
-typedef enum { MLA_BF16 = 0, MLA_FP32 = 1, MLA_FP8_CACHE = 2 } mla_dtype_t;
+ * divided by s_t (see mla_decode_run_fp8). Tensor-core path, one latent shard.
+ * MLA_FP16 is a type of the grouped-head operators (mla_paged.h) only. */
+typedef enum { MLA_BF16 = 0, MLA_FP32 = 1, MLA_FP8_CACHE = 2, MLA_FP16 = 3 } mla_dtype_t;
 
 /* Kernel family selection (mla_plan_options_t.kernel). */
 typedef enum {

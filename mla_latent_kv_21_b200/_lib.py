@@ -1,6 +1,6 @@
 """ctypes binding of libmla_decode.so (argument marshalling only).
 
-Every function keeps the C name from include/mla_decode.h. Device buffers are
+Every function keeps the C name from include/mla_decode.h or mla_paged.h. Device buffers are
 passed as integer addresses (e.g. ``tensor.data_ptr()``), streams as integer
 handles (``torch.cuda.current_stream().cuda_stream``). A non-OK status raises
 MlaError. There is no fallback: if the library is missing, importing this
@@ -35,12 +35,16 @@ MLA_ERR_NO_DEVICE = 7
 MLA_BF16 = 0
 MLA_FP32 = 1
 MLA_FP8_CACHE = 2
+MLA_FP16 = 3
+
+MLA_ROPE_HALF = 0
+MLA_ROPE_INTERLEAVED = 1
 
 MLA_KERNEL_AUTO = 0
 MLA_KERNEL_SIMT = 1
 MLA_KERNEL_TCGEN05 = 2
 
-# symbols declared in include/mla_decode.h
+# symbols declared in include/mla_decode.h and include/mla_paged.h
 EXPORTED = (
     "mla_decode_plan", "mla_decode_plan_ex", "mla_decode_run", "mla_decode_run_ex",
     "mla_decode_run_fp8", "mla_decode_run_no_alloc", "mla_decode_selftest_timeout", "mla_decode_run_blasst",
@@ -48,6 +52,9 @@ EXPORTED = (
     "mla_decode_read_status", "mla_plan_get_info", "mla_plan_segments", "mla_plan_destroy",
     "mla_status_string", "mla_abi_version", "mla_prefill_plan", "mla_prefill_run",
     "mla_prefill_run_ex", "mla_prefill_plan_destroy",
+    "mla_gqa_append", "mla_latent_append",
+    "mla_gqa_decode_plan", "mla_gqa_decode_run", "mla_gqa_decode_plan_destroy",
+    "mla_gqa_prefill_plan", "mla_gqa_prefill_run", "mla_gqa_prefill_plan_destroy",
 )
 
 
@@ -77,6 +84,32 @@ class mla_plan_info_t(ctypes.Structure):
 
 _vp, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _i32p = ctypes.POINTER(ctypes.c_int32)
+
+
+class mla_gqa_dims_t(ctypes.Structure):
+    _fields_ = [("num_q_heads", _i32), ("num_kv_heads", _i32), ("head_dim", _i32), ("q_len", _i32),
+                ("page_size", _i32), ("rope_dim", _i32), ("rope_style", _i32), ("dtype", _i32),
+                ("softmax_scale", ctypes.c_float)]
+
+
+class mla_gqa_append_args_t(ctypes.Structure):
+    _fields_ = [("k", _vp), ("k_token_stride", _i64), ("k_head_stride", _i64),
+                ("v", _vp), ("v_token_stride", _i64), ("v_head_stride", _i64),
+                ("q", _vp), ("q_token_stride", _i64), ("q_head_stride", _i64),
+                ("q_out", _vp), ("k_pool", _vp), ("v_pool", _vp), ("num_blocks", _i64),
+                ("block_table", _vp), ("block_table_stride", _i32), ("batch", _i32),
+                ("seq_lens", _vp), ("cu_seqlens", _vp), ("num_tokens", _i64),
+                ("rope_table", _vp), ("rope_positions", _i64)]
+
+
+class mla_latent_append_args_t(ctypes.Structure):
+    _fields_ = [("ckv", _vp), ("ckv_token_stride", _i64), ("k_rope", _vp), ("k_rope_token_stride", _i64),
+                ("q_rope", _vp), ("q_rope_token_stride", _i64), ("q_rope_head_stride", _i64),
+                ("q_rope_out", _vp), ("kv_pool", _vp), ("kv_rope", _vp), ("kv_scale", _vp), ("kv_rows", _vp),
+                ("num_blocks", _i64), ("block_table", _vp), ("block_table_stride", _i32), ("batch", _i32),
+                ("seq_lens", _vp), ("cu_seqlens", _vp), ("num_tokens", _i64),
+                ("rope_table", _vp), ("rope_positions", _i64)]
+
 
 _lib.mla_status_string.restype = ctypes.c_char_p
 _lib.mla_status_string.argtypes = [ctypes.c_int]
@@ -117,6 +150,25 @@ _lib.mla_prefill_run_ex.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                     ctypes.POINTER(mla_run_options_t)]
 _lib.mla_prefill_plan_destroy.restype = None
 _lib.mla_prefill_plan_destroy.argtypes = [_vp]
+_lib.mla_gqa_append.restype = ctypes.c_int
+_lib.mla_gqa_append.argtypes = [ctypes.POINTER(mla_gqa_dims_t), ctypes.POINTER(mla_gqa_append_args_t), _vp, _sz, _vp]
+_lib.mla_latent_append.restype = ctypes.c_int
+_lib.mla_latent_append.argtypes = [ctypes.POINTER(mla_dims_t), _i32, ctypes.POINTER(mla_latent_append_args_t), _vp,
+                                   _sz, _vp]
+_lib.mla_gqa_decode_plan.restype = ctypes.c_int
+_lib.mla_gqa_decode_plan.argtypes = [ctypes.POINTER(mla_gqa_dims_t), _i32, _i32p, ctypes.POINTER(mla_plan_options_t),
+                                     ctypes.POINTER(_vp), ctypes.POINTER(_sz)]
+_lib.mla_gqa_decode_run.restype = ctypes.c_int
+_lib.mla_gqa_decode_run.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _sz, _vp]
+_lib.mla_gqa_decode_plan_destroy.restype = None
+_lib.mla_gqa_decode_plan_destroy.argtypes = [_vp]
+_lib.mla_gqa_prefill_plan.restype = ctypes.c_int
+_lib.mla_gqa_prefill_plan.argtypes = [ctypes.POINTER(mla_gqa_dims_t), _i32, _i32p, ctypes.POINTER(_vp),
+                                      ctypes.POINTER(_sz)]
+_lib.mla_gqa_prefill_run.restype = ctypes.c_int
+_lib.mla_gqa_prefill_run.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.mla_gqa_prefill_plan_destroy.restype = None
+_lib.mla_gqa_prefill_plan_destroy.argtypes = [_vp]
 _lib.mla_workspace_init.restype = ctypes.c_int
 _lib.mla_workspace_init.argtypes = [_vp, _sz, _vp]
 _lib.mla_decode_read_status.restype = ctypes.c_int
@@ -264,6 +316,55 @@ def mla_prefill_run(plan, q_nope, q_rope, kv_rows, cu_seqlens, w_uk, w_uv, out, 
 
 def mla_prefill_plan_destroy(plan) -> None:
     _lib.mla_prefill_plan_destroy(plan)
+
+
+def mla_gqa_append(dims: mla_gqa_dims_t, args: mla_gqa_append_args_t, workspace, workspace_bytes, stream=0) -> None:
+    _check(_lib.mla_gqa_append(ctypes.byref(dims), ctypes.byref(args), workspace, workspace_bytes, stream),
+           "mla_gqa_append")
+
+
+def mla_latent_append(dims: mla_dims_t, rope_style: int, args: mla_latent_append_args_t, workspace, workspace_bytes,
+                      stream=0) -> None:
+    _check(_lib.mla_latent_append(ctypes.byref(dims), rope_style, ctypes.byref(args), workspace, workspace_bytes,
+                                  stream), "mla_latent_append")
+
+
+def mla_gqa_decode_plan(dims: mla_gqa_dims_t, seq_lens_host: Sequence[int], num_sms: int = 0, num_workers: int = 0):
+    """Returns (plan handle, workspace bytes)."""
+    plan, ws = _vp(), _sz()
+    opts = mla_plan_options_t(num_sms, MLA_KERNEL_AUTO, num_workers)
+    _check(_lib.mla_gqa_decode_plan(ctypes.byref(dims), len(seq_lens_host), _lens_array(seq_lens_host),
+                                    ctypes.byref(opts), ctypes.byref(plan), ctypes.byref(ws)), "mla_gqa_decode_plan")
+    return plan.value, ws.value
+
+
+def mla_gqa_decode_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride, seq_lens_dev, out,
+                       workspace, workspace_bytes, stream=0) -> None:
+    _check(_lib.mla_gqa_decode_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride,
+                                   seq_lens_dev, out, workspace, workspace_bytes, stream), "mla_gqa_decode_run")
+
+
+def mla_gqa_decode_plan_destroy(plan) -> None:
+    _lib.mla_gqa_decode_plan_destroy(plan)
+
+
+def mla_gqa_prefill_plan(dims: mla_gqa_dims_t, new_tokens_host: Sequence[int]):
+    """Returns (plan handle, workspace bytes)."""
+    plan, ws = _vp(), _sz()
+    _check(_lib.mla_gqa_prefill_plan(ctypes.byref(dims), len(new_tokens_host), _lens_array(new_tokens_host),
+                                     ctypes.byref(plan), ctypes.byref(ws)), "mla_gqa_prefill_plan")
+    return plan.value, ws.value
+
+
+def mla_gqa_prefill_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride, cu_seqlens_dev,
+                        seq_lens_dev, out, workspace, workspace_bytes, stream=0) -> None:
+    _check(_lib.mla_gqa_prefill_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride,
+                                    cu_seqlens_dev, seq_lens_dev, out, workspace, workspace_bytes, stream),
+           "mla_gqa_prefill_run")
+
+
+def mla_gqa_prefill_plan_destroy(plan) -> None:
+    _lib.mla_gqa_prefill_plan_destroy(plan)
 
 
 def mla_workspace_init(workspace, workspace_bytes, stream=0) -> None:

@@ -8,7 +8,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmla_decode.so")
-SOURCES = ["mla_decode_api.cu", "no_alloc.cu"]
+SOURCES = ["mla_decode_api.cu", "no_alloc.cu", "paged_api.cu"]
 GENCODE = "-gencode=arch=compute_100a,code=sm_100a"
 
 
@@ -24,7 +24,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "mla_decode.h"))
+    deps += [os.path.join(HERE, "..", "include", f) for f in ("mla_decode.h", "mla_paged.h")]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
 
 
@@ -32,7 +32,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not _stale():
         return LIB
     cmd = [nvcc_path(), GENCODE, "-lineinfo", "-O3", "-std=c++17", "--expt-relaxed-constexpr",
-           "-Xcompiler", "-fPIC", "-shared", "-o", LIB + ".tmp",
+           "-t", "0", "-Xcompiler", "-fPIC", "-shared", "-o", LIB + ".tmp",
            *[os.path.join(CSRC, s) for s in SOURCES], *extra]
     if verbose:
         print(" ".join(cmd), file=sys.stderr)

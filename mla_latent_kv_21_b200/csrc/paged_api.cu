@@ -1,0 +1,327 @@
+// Host side of the paged-cache operators (include/mla_paged.h): checks of the
+// arguments, plans, launches.
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "paged_append.cuh"
+#include "paged_attend.cuh"
+
+using namespace mla;
+
+struct mla_gqa_decode_plan {
+  mla_gqa_dims_t dims;
+  int32_t B, W;
+  size_t o_off, ml_off, total;
+};
+
+struct mla_gqa_prefill_plan {
+  mla_gqa_dims_t dims;
+  int32_t B, max_new;
+  int64_t T;
+};
+
+namespace {
+
+constexpr size_t kHeaderBytes = 1024;
+
+mla_status_t check_dims(const mla_gqa_dims_t& d) {
+  if (d.num_q_heads < 1 || d.num_kv_heads < 1 || d.num_q_heads % d.num_kv_heads != 0 || d.head_dim < 1 ||
+      d.q_len < 1 || d.rope_dim < 0 || d.rope_dim > d.head_dim || !std::isfinite(d.softmax_scale) ||
+      d.softmax_scale <= 0.f || (d.rope_style != MLA_ROPE_HALF && d.rope_style != MLA_ROPE_INTERLEAVED))
+    return MLA_ERR_INVALID_ARG;
+  if (d.dtype != MLA_BF16 && d.dtype != MLA_FP16)
+    return d.dtype == MLA_FP32 || d.dtype == MLA_FP8_CACHE ? MLA_ERR_UNSUPPORTED : MLA_ERR_INVALID_ARG;
+  if ((d.head_dim != 64 && d.head_dim != 128) || d.page_size != 64 || d.rope_dim % 16 != 0 || d.num_q_heads > 4096)
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool multiple(int64_t a, int64_t b, int64_t n) { return a % n == 0 && b % n == 0; }
+
+mla_status_t launched() { return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+
+// Rows of the cache and of the batch: tensor-map and grid coordinates are 32-bit.
+bool fits32(int64_t rows) { return rows < (int64_t(1) << 31); }
+
+}  // namespace
+
+extern "C" {
+
+mla_status_t mla_gqa_append(const mla_gqa_dims_t* dims, const mla_gqa_append_args_t* args, void* workspace,
+                            size_t workspace_bytes, void* stream_) {
+  if (!dims || !args || !workspace) return MLA_ERR_INVALID_ARG;
+  const mla_gqa_dims_t& d = *dims;
+  const mla_gqa_append_args_t& a = *args;
+  const mla_status_t st = check_dims(d);
+  if (st != MLA_OK) return st;
+  if (workspace_bytes < kHeaderBytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (a.batch < 1 || a.num_tokens < 0 || a.num_blocks < 1 || a.block_table_stride < 1 || a.rope_positions < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!a.cu_seqlens && a.num_tokens != (int64_t)a.batch * d.q_len) return MLA_ERR_INVALID_ARG;
+  if (a.num_tokens == 0) return MLA_OK;
+  if (!a.k || !a.v || !a.k_pool || !a.v_pool || !a.block_table || !a.seq_lens || (a.q && !a.q_out) ||
+      (d.rope_dim > 0 && !a.rope_table))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(a.k) || !aligned16(a.v) || !aligned16(a.q) || !aligned16(a.q_out) || !aligned16(a.k_pool) ||
+      !aligned16(a.v_pool) || !aligned16(a.rope_table) || !multiple(a.k_token_stride, a.k_head_stride, 8) ||
+      !multiple(a.v_token_stride, a.v_head_stride, 8) || (a.q && !multiple(a.q_token_stride, a.q_head_stride, 8)))
+    return MLA_ERR_INVALID_ARG;
+  if (!fits32(a.num_tokens) || !fits32(a.num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  AppendParams p{};
+  p.k = a.k; p.k_ts = a.k_token_stride; p.k_hs = a.k_head_stride;
+  p.v = a.v; p.v_ts = a.v_token_stride; p.v_hs = a.v_head_stride;
+  p.q = a.q; p.q_ts = a.q_token_stride; p.q_hs = a.q_head_stride;
+  p.q_out = a.q_out;
+  p.k_pool = a.k_pool;
+  p.v_pool = a.v_pool;
+  p.status = static_cast<int32_t*>(workspace);
+  p.block_table = a.block_table;
+  p.bt_stride = a.block_table_stride;
+  p.seq_lens = a.seq_lens;
+  p.cu = a.cu_seqlens;
+  p.table = a.rope_table;
+  p.table_rows = a.rope_positions;
+  p.num_blocks = a.num_blocks;
+  p.T = a.num_tokens;
+  p.B = a.batch;
+  p.Lq = d.q_len;
+  p.Hq = d.num_q_heads;
+  p.Hk = d.num_kv_heads;
+  p.d = d.head_dim;
+  p.D = d.rope_dim;
+  const int H = (a.q ? p.Hq : 0) + 2 * p.Hk, tokens = pg::kAppendThreads / (p.d / 16);
+  const int64_t gx = (p.T + tokens - 1) / tokens;
+  // a thread's heads: 16 where that still fills the machine, else 4 (one batch
+  // of loads)
+  p.heads_per_cta = gx * ((H + 15) / 16) >= 1184 ? 16 : 4;
+  const dim3 grid((unsigned)gx, (unsigned)((H + p.heads_per_cta - 1) / p.heads_per_cta));
+  const int half = d.rope_style == MLA_ROPE_HALF;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  if (d.dtype == MLA_BF16) pg::gqa_append_kernel<__nv_bfloat16><<<grid, pg::kAppendThreads, 0, stream>>>(p, half);
+  else pg::gqa_append_kernel<__half><<<grid, pg::kAppendThreads, 0, stream>>>(p, half);
+  return launched();
+}
+
+mla_status_t mla_latent_append(const mla_dims_t* dims, int32_t rope_style, const mla_latent_append_args_t* args,
+                               void* workspace, size_t workspace_bytes, void* stream_) {
+  if (!dims || !args || !workspace) return MLA_ERR_INVALID_ARG;
+  const mla_dims_t& d = *dims;
+  const mla_latent_append_args_t& a = *args;
+  if (d.num_heads < 1 || d.latent_rank < 1 || d.rope_dim < 0 || d.q_len < 1 ||
+      (rope_style != MLA_ROPE_HALF && rope_style != MLA_ROPE_INTERLEAVED))
+    return MLA_ERR_INVALID_ARG;
+  if (d.dtype != MLA_BF16 && d.dtype != MLA_FP32 && d.dtype != MLA_FP8_CACHE) return MLA_ERR_INVALID_ARG;
+  const bool fp8 = d.dtype == MLA_FP8_CACHE;
+  if (d.page_size != 64 || d.rope_dim % 2 != 0 || d.latent_rank > 512 || d.latent_rank + d.rope_dim > 576 ||
+      d.num_heads > 4096 || (fp8 && (d.latent_rank != 512 || d.rope_dim != 64)))
+    return MLA_ERR_UNSUPPORTED;
+  if (workspace_bytes < kHeaderBytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (a.batch < 1 || a.num_tokens < 0 || a.num_blocks < 1 || a.block_table_stride < 1 || a.rope_positions < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (!a.cu_seqlens && a.num_tokens != (int64_t)a.batch * d.q_len) return MLA_ERR_INVALID_ARG;
+  if (a.num_tokens == 0) return MLA_OK;
+  const bool rot = d.rope_dim > 0;
+  if (!a.ckv || !a.kv_pool || !a.block_table || !a.seq_lens || (rot && (!a.k_rope || !a.rope_table)) ||
+      (a.q_rope && (!rot || !a.q_rope_out)) || (fp8 && (!a.kv_rope || !a.kv_scale)))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(a.rope_table)) return MLA_ERR_INVALID_ARG;
+  const int V = d.dtype == MLA_FP32 ? 4 : 8;
+  const bool wide = aligned16(a.ckv) && aligned16(a.k_rope) && aligned16(a.q_rope) && aligned16(a.q_rope_out) &&
+                    aligned16(a.kv_pool) && aligned16(a.kv_rope) && aligned16(a.kv_rows) && d.latent_rank % V == 0 &&
+                    d.rope_dim % (2 * V) == 0 && a.ckv_token_stride % V == 0 &&
+                    (!rot || a.k_rope_token_stride % V == 0) &&
+                    (!a.q_rope || multiple(a.q_rope_token_stride, a.q_rope_head_stride, V));
+  if (fp8 && !wide) return MLA_ERR_INVALID_ARG;
+  if (!fits32(a.num_tokens) || !fits32(a.num_blocks)) return MLA_ERR_UNSUPPORTED;
+  AppendParams p{};
+  p.k = a.ckv; p.k_ts = a.ckv_token_stride;
+  p.v = a.k_rope; p.v_ts = a.k_rope_token_stride;
+  p.q = a.q_rope; p.q_ts = a.q_rope_token_stride; p.q_hs = a.q_rope_head_stride;
+  p.q_out = a.q_rope_out;
+  p.k_pool = a.kv_pool;
+  p.v_pool = a.kv_rope;
+  p.kv_scale = a.kv_scale;
+  p.kv_rows = a.kv_rows;
+  p.status = static_cast<int32_t*>(workspace);
+  p.block_table = a.block_table;
+  p.bt_stride = a.block_table_stride;
+  p.seq_lens = a.seq_lens;
+  p.cu = a.cu_seqlens;
+  p.table = a.rope_table;
+  p.table_rows = a.rope_positions;
+  p.num_blocks = a.num_blocks;
+  p.T = a.num_tokens;
+  p.B = a.batch;
+  p.Lq = d.q_len;
+  p.Hq = d.num_heads;
+  p.D = d.rope_dim;
+  p.r = d.latent_rank;
+  const int half = rope_style == MLA_ROPE_HALF;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const dim3 grid((unsigned)p.T);
+  const int n = pg::kLatentThreads;
+  if (fp8) pg::latent_append_kernel<__nv_bfloat16, true><<<grid, n, 0, stream>>>(p, half);
+  else if (wide && d.dtype == MLA_BF16) pg::latent_append_kernel<__nv_bfloat16, false><<<grid, n, 0, stream>>>(p, half);
+  else if (wide) pg::latent_append_kernel<float, false><<<grid, n, 0, stream>>>(p, half);
+  else if (d.dtype == MLA_BF16) pg::latent_append_narrow_kernel<__nv_bfloat16><<<grid, n, 0, stream>>>(p, half);
+  else pg::latent_append_narrow_kernel<float><<<grid, n, 0, stream>>>(p, half);
+  return launched();
+}
+
+mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, const int32_t* seq_lens_host,
+                                 const mla_plan_options_t* opts, mla_gqa_decode_plan_t* plan_out,
+                                 size_t* workspace_bytes) {
+  if (!dims || !seq_lens_host || !plan_out || batch < 1) return MLA_ERR_INVALID_ARG;
+  *plan_out = nullptr;
+  const mla_status_t st = check_dims(*dims);
+  if (st != MLA_OK) return st;
+  const mla_gqa_dims_t& d = *dims;
+  const int G = d.num_q_heads / d.num_kv_heads;
+  if ((int64_t)G * d.q_len > 64 || !fits32((int64_t)batch * d.q_len * d.num_q_heads)) return MLA_ERR_UNSUPPORTED;
+  mla_plan_options_t o{};
+  if (opts) o = *opts;
+  int32_t sms = o.num_sms;
+  if (sms < 0 || o.num_workers < 0 || o.kernel != MLA_KERNEL_AUTO) return MLA_ERR_INVALID_ARG;
+  if (sms == 0) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+      (void)cudaGetLastError();
+      return MLA_ERR_NO_DEVICE;
+    }
+  }
+  int64_t pages = 0;
+  for (int b = 0; b < batch; ++b) {
+    if (seq_lens_host[b] < 0) return MLA_ERR_INVALID_ARG;
+    pages += ceil_div64(seq_lens_host[b], pg::kPage) * d.num_kv_heads;
+  }
+  const int64_t most = o.num_workers > 0 ? o.num_workers : 2 * sms;
+  struct mla_gqa_decode_plan* p = new (std::nothrow) struct mla_gqa_decode_plan();
+  if (!p) return MLA_ERR_INVALID_ARG;
+  p->dims = d;
+  p->B = batch;
+  p->W = (int32_t)std::max<int64_t>(1, std::min<int64_t>({most, pages, 4096}));
+  const size_t rows = (size_t)2 * p->W * G * d.q_len;
+  p->o_off = kHeaderBytes;
+  p->ml_off = align_up(p->o_off + rows * d.head_dim * sizeof(float), 1024);
+  p->total = align_up(p->ml_off + rows * 2 * sizeof(float), 1024);
+  *plan_out = p;
+  if (workspace_bytes) *workspace_bytes = p->total;
+  return MLA_OK;
+}
+
+mla_status_t mla_gqa_decode_run(mla_gqa_decode_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
+                                int64_t num_blocks, const int32_t* block_table, int32_t block_table_stride,
+                                const int32_t* seq_lens_dev, void* out, void* workspace, size_t workspace_bytes,
+                                void* stream_) {
+  if (!plan || !q || !k_pool || !v_pool || !block_table || !seq_lens_dev || !out || !workspace || num_blocks < 1 ||
+      block_table_stride < 1 || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < plan->total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const mla_gqa_dims_t& d = plan->dims;
+  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  char* ws = static_cast<char*>(workspace);
+  GqaParams p{};
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.out = out;
+  p.status = reinterpret_cast<int32_t*>(ws);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens_dev;
+  p.o_part = reinterpret_cast<float*>(ws + plan->o_off);
+  p.ml_part = reinterpret_cast<float*>(ws + plan->ml_off);
+  p.num_blocks = num_blocks;
+  p.bt_stride = block_table_stride;
+  p.B = plan->B;
+  p.Lq = d.q_len;
+  p.T = (int64_t)plan->B * d.q_len;
+  p.Hq = d.num_q_heads;
+  p.Hk = d.num_kv_heads;
+  p.G = p.Hq / p.Hk;
+  p.W = plan->W;
+  p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const dim3 grid((unsigned)p.T, (unsigned)p.Hq);
+  const bool bf = d.dtype == MLA_BF16;
+  if (bf && d.head_dim == 128) pg::attend_row_kernel<__nv_bfloat16, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  else if (bf) pg::attend_row_kernel<__nv_bfloat16, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  else if (d.head_dim == 128) pg::attend_row_kernel<__half, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  else pg::attend_row_kernel<__half, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  return launched();
+}
+
+void mla_gqa_decode_plan_destroy(mla_gqa_decode_plan_t plan) { delete plan; }
+
+mla_status_t mla_gqa_prefill_plan(const mla_gqa_dims_t* dims, int32_t batch, const int32_t* new_tokens_host,
+                                  mla_gqa_prefill_plan_t* plan_out, size_t* workspace_bytes) {
+  if (!dims || !new_tokens_host || !plan_out || batch < 1) return MLA_ERR_INVALID_ARG;
+  *plan_out = nullptr;
+  const mla_status_t st = check_dims(*dims);
+  if (st != MLA_OK) return st;
+  const mla_gqa_dims_t& d = *dims;
+  int64_t T = 0;
+  int32_t most = 0;
+  for (int b = 0; b < batch; ++b) {
+    if (new_tokens_host[b] < 0) return MLA_ERR_INVALID_ARG;
+    T += new_tokens_host[b];
+    most = std::max(most, new_tokens_host[b]);
+  }
+  if (d.num_q_heads / d.num_kv_heads > 128 || !fits32(T + 256) || batch > 65535) return MLA_ERR_UNSUPPORTED;
+  struct mla_gqa_prefill_plan* p = new (std::nothrow) struct mla_gqa_prefill_plan();
+  if (!p) return MLA_ERR_INVALID_ARG;
+  p->dims = d;
+  p->B = batch;
+  p->T = T;
+  p->max_new = most;
+  *plan_out = p;
+  if (workspace_bytes) *workspace_bytes = kHeaderBytes;
+  return MLA_OK;
+}
+
+mla_status_t mla_gqa_prefill_run(mla_gqa_prefill_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
+                                 int64_t num_blocks, const int32_t* block_table, int32_t block_table_stride,
+                                 const int32_t* cu_seqlens_dev, const int32_t* seq_lens_dev, void* out,
+                                 void* workspace, size_t workspace_bytes, void* stream_) {
+  if (!plan || !workspace || num_blocks < 1 || block_table_stride < 1) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < kHeaderBytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (plan->T == 0) return MLA_OK;
+  if (!q || !k_pool || !v_pool || !block_table || !cu_seqlens_dev || !seq_lens_dev || !out || !aligned16(q) ||
+      !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return MLA_ERR_INVALID_ARG;
+  const mla_gqa_dims_t& d = plan->dims;
+  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  GqaParams p{};
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.out = out;
+  p.status = static_cast<int32_t*>(workspace);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens_dev;
+  p.cu = cu_seqlens_dev;
+  p.num_blocks = num_blocks;
+  p.bt_stride = block_table_stride;
+  p.B = plan->B;
+  p.T = plan->T;
+  p.Hq = d.num_q_heads;
+  p.Hk = d.num_kv_heads;
+  p.G = p.Hq / p.Hk;
+  p.max_new = plan->max_new;
+  p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const dim3 grid((unsigned)p.T, (unsigned)p.Hq);
+  const bool bf = d.dtype == MLA_BF16;
+  if (bf && d.head_dim == 128) pg::attend_row_kernel<__nv_bfloat16, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  else if (bf) pg::attend_row_kernel<__nv_bfloat16, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  else if (d.head_dim == 128) pg::attend_row_kernel<__half, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  else pg::attend_row_kernel<__half, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
+  return launched();
+}
+
+void mla_gqa_prefill_plan_destroy(mla_gqa_prefill_plan_t plan) { delete plan; }
+
+}  // extern "C"

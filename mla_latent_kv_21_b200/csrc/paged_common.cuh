@@ -1,0 +1,61 @@
+// Shared definitions of the paged-cache operators (include/mla_paged.h): types
+// and conversions, the lookup of a packed token's sequence, tensor maps.
+#pragma once
+
+#include "../../include/mla_paged.h"
+#include "common.cuh"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace pg {
+
+constexpr int kPage = 64;   // tokens per cache block
+
+template <typename T> struct Pack;   // two values of a 16-bit type in 32 bits
+template <> struct Pack<__nv_bfloat16> {
+  static __device__ __forceinline__ uint32_t of(float lo, float hi) {
+    __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  static __device__ __forceinline__ float2 to(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  }
+};
+template <> struct Pack<__half> {
+  static __device__ __forceinline__ uint32_t of(float lo, float hi) { return ptx::cvt_f16x2(lo, hi); }
+  static __device__ __forceinline__ float2 to(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
+};
+
+// The sequence b with cu[b] <= t < cu[b + 1] of a packed token t, or -1 for a
+// row that belongs to none. The prefix sums (or every `step`-th of them, where
+// there are more than kCuShared) are in shared memory: a search over global
+// memory would cost a dependent L2 round trip per halving.
+constexpr int kCuShared = 1024;
+struct CuSearch {
+  const int32_t* cu;       // global, [B + 1]
+  int32_t B, step, n;      // n samples cu[0], cu[step], ..
+};
+__device__ __forceinline__ CuSearch stage_cu(const int32_t* cu, int32_t B, int32_t* shared) {
+  CuSearch s{cu, B, B / kCuShared + 1, 0};
+  s.n = B / s.step + 1;
+  for (int i = threadIdx.x; i < s.n; i += blockDim.x) shared[i] = cu[i * s.step];
+  return s;   // the caller synchronises the block
+}
+__device__ __forceinline__ int32_t sequence_of(const CuSearch& s, const int32_t* shared, int32_t t) {
+  int lo = 0, hi = s.n - 1;   // the last sample <= t
+  if (shared[0] > t) return -1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (shared[mid] <= t) lo = mid; else hi = mid - 1;
+  }
+  if (s.step == 1) return lo < s.B ? lo : -1;
+  int a = lo * s.step, e = min(a + s.step - 1, s.B);
+  while (a < e) {
+    const int mid = (a + e + 1) >> 1;
+    if (s.cu[mid] <= t) a = mid; else e = mid - 1;
+  }
+  return a < s.B ? a : -1;
+}
+
+}  // namespace pg
+}  // namespace mla
