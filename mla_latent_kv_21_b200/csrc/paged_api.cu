@@ -3,16 +3,18 @@
 #include <algorithm>
 #include <cmath>
 #include <new>
+#include <type_traits>
 
 #include "paged_append.cuh"
 #include "paged_attend.cuh"
+#include "paged_decode.cuh"
 
 using namespace mla;
 
 struct mla_gqa_decode_plan {
   mla_gqa_dims_t dims;
   int32_t B, W;
-  size_t o_off, ml_off, total;
+  size_t o_off, ml_off, tails_off, total;
 };
 
 struct mla_gqa_prefill_plan {
@@ -41,7 +43,11 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 
 bool multiple(int64_t a, int64_t b, int64_t n) { return a % n == 0 && b % n == 0; }
 
-mla_status_t launched() { return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA; }
+// A failed launch leaves no error behind for a later call to find.
+mla_status_t launched(cudaError_t e = cudaSuccess) {
+  const cudaError_t last = cudaGetLastError();
+  return e == cudaSuccess && last == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
 
 // Rows of the cache and of the batch: tensor-map and grid coordinates are 32-bit.
 bool fits32(int64_t rows) { return rows < (int64_t(1) << 31); }
@@ -207,7 +213,8 @@ mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, cons
   const size_t rows = (size_t)2 * p->W * G * d.q_len;
   p->o_off = kHeaderBytes;
   p->ml_off = align_up(p->o_off + rows * d.head_dim * sizeof(float), 1024);
-  p->total = align_up(p->ml_off + rows * 2 * sizeof(float), 1024);
+  p->tails_off = align_up(p->ml_off + rows * sizeof(float2), 1024);
+  p->total = align_up(p->tails_off + p->W * sizeof(int2), 1024);
   *plan_out = p;
   if (workspace_bytes) *workspace_bytes = p->total;
   return MLA_OK;
@@ -233,7 +240,9 @@ mla_status_t mla_gqa_decode_run(mla_gqa_decode_plan_t plan, const void* q, const
   p.block_table = block_table;
   p.seq_lens = seq_lens_dev;
   p.o_part = reinterpret_cast<float*>(ws + plan->o_off);
-  p.ml_part = reinterpret_cast<float*>(ws + plan->ml_off);
+  p.ml_part = reinterpret_cast<float2*>(ws + plan->ml_off);
+  p.tails = reinterpret_cast<int2*>(ws + plan->tails_off);
+  p.wait_limit_ns = ptx::kWaitLimitNs;
   p.num_blocks = num_blocks;
   p.bt_stride = block_table_stride;
   p.B = plan->B;
@@ -245,13 +254,13 @@ mla_status_t mla_gqa_decode_run(mla_gqa_decode_plan_t plan, const void* q, const
   p.W = plan->W;
   p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const dim3 grid((unsigned)p.T, (unsigned)p.Hq);
+  const int64_t items = (int64_t)p.B * p.Hk;
   const bool bf = d.dtype == MLA_BF16;
-  if (bf && d.head_dim == 128) pg::attend_row_kernel<__nv_bfloat16, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  else if (bf) pg::attend_row_kernel<__nv_bfloat16, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  else if (d.head_dim == 128) pg::attend_row_kernel<__half, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  else pg::attend_row_kernel<__half, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  return launched();
+  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_decode<__nv_bfloat16, 128>(p, items, stream)
+                      : bf                      ? pg::launch_decode<__nv_bfloat16, 64>(p, items, stream)
+                      : d.head_dim == 128       ? pg::launch_decode<__half, 128>(p, items, stream)
+                                                : pg::launch_decode<__half, 64>(p, items, stream);
+  return launched(e);
 }
 
 void mla_gqa_decode_plan_destroy(mla_gqa_decode_plan_t plan) { delete plan; }

@@ -8,23 +8,6 @@
 
 namespace mla {
 
-struct GqaParams {
-  const void* q;           // [T, Hq, d]
-  const void* k_pool;      // [num_blocks, Hk, 64, d]
-  const void* v_pool;
-  void* out;               // [T, Hq, d]
-  int32_t* status;
-  const int32_t* block_table;
-  const int32_t* seq_lens;
-  const int32_t* cu;       // prefill; NULL: Lq queries per sequence
-  float* o_part;           // decode workspace
-  float* ml_part;
-  int64_t num_blocks, T;
-  int32_t bt_stride, B, Lq, Hq, Hk, G, W;
-  int32_t max_new;         // prefill: largest count of the plan
-  float scale_log2;
-};
-
 namespace pg {
 
 constexpr int kRowThreads = 128;

@@ -26,6 +26,30 @@ template <> struct Pack<__half> {
   static __device__ __forceinline__ float2 to(uint32_t v) { return __half22float2(*reinterpret_cast<__half2*>(&v)); }
 };
 
+// ------------------------------------------------------------ parameters -----
+}  // namespace pg
+
+struct GqaParams {
+  const void* q;           // [T, Hq, d]
+  const void* k_pool;      // [num_blocks, Hk, 64, d]
+  const void* v_pool;
+  void* out;               // [T, Hq, d]
+  int32_t* status;
+  const int32_t* block_table;
+  const int32_t* seq_lens;
+  const int32_t* cu;       // prefill
+  float* o_part;           // decode workspace: partial sums of split items
+  float2* ml_part;         // their running maxima and sums
+  int2* tails;             // per worker, the item it began and did not finish
+  int64_t num_blocks, T;
+  int32_t bt_stride, B, Lq, Hq, Hk, G, W;
+  int32_t max_new;         // prefill: largest count of the plan
+  float scale_log2;
+  uint64_t wait_limit_ns;
+};
+
+namespace pg {
+
 // The sequence b with cu[b] <= t < cu[b + 1] of a packed token t, or -1 for a
 // row that belongs to none. The prefix sums (or every `step`-th of them, where
 // there are more than kCuShared) are in shared memory: a search over global
@@ -55,6 +79,36 @@ __device__ __forceinline__ int32_t sequence_of(const CuSearch& s, const int32_t*
     if (s.cu[mid] <= t) a = mid; else e = mid - 1;
   }
   return a < s.B ? a : -1;
+}
+
+// ------------------------------------------------------------ tensor maps ----
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeTiledFn encode_fn() {
+  static EncodeTiledFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiledFn>(nullptr);
+    return reinterpret_cast<EncodeTiledFn>(f);
+  }();
+  return fn;
+}
+
+// A pool [num_blocks * Hk, 64, d] of a 16-bit type as (d, 64, pages): boxes of
+// 64 columns of one page, rows of 128 bytes in the 128-byte swizzle.
+inline bool pool_map(CUtensorMap* m, const void* pool, int64_t pages, int d, bool bf16) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[3] = {(cuuint64_t)d, kPage, (cuuint64_t)pages};
+  const cuuint64_t strides[2] = {(cuuint64_t)d * 2, (cuuint64_t)d * 2 * kPage};
+  const cuuint32_t box[3] = {64, kPage, 1}, es[3] = {1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(pool),
+             dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace pg
