@@ -6,8 +6,8 @@
 #include <type_traits>
 
 #include "paged_append.cuh"
-#include "paged_attend.cuh"
 #include "paged_decode.cuh"
+#include "paged_prefill.cuh"
 
 using namespace mla;
 
@@ -279,7 +279,10 @@ mla_status_t mla_gqa_prefill_plan(const mla_gqa_dims_t* dims, int32_t batch, con
     T += new_tokens_host[b];
     most = std::max(most, new_tokens_host[b]);
   }
-  if (d.num_q_heads / d.num_kv_heads > 128 || !fits32(T + 256) || batch > 65535) return MLA_ERR_UNSUPPORTED;
+  const int G = d.num_q_heads / d.num_kv_heads;
+  if (G > 128 || !fits32(T + 2 * pg::kTile) ||
+      !fits32(pg::prefill_steps(most, G) * batch * d.num_kv_heads))
+    return MLA_ERR_UNSUPPORTED;
   struct mla_gqa_prefill_plan* p = new (std::nothrow) struct mla_gqa_prefill_plan();
   if (!p) return MLA_ERR_INVALID_ARG;
   p->dims = d;
@@ -321,14 +324,14 @@ mla_status_t mla_gqa_prefill_run(mla_gqa_prefill_plan_t plan, const void* q, con
   p.G = p.Hq / p.Hk;
   p.max_new = plan->max_new;
   p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
+  p.wait_limit_ns = ptx::kWaitLimitNs;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const dim3 grid((unsigned)p.T, (unsigned)p.Hq);
   const bool bf = d.dtype == MLA_BF16;
-  if (bf && d.head_dim == 128) pg::attend_row_kernel<__nv_bfloat16, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  else if (bf) pg::attend_row_kernel<__nv_bfloat16, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  else if (d.head_dim == 128) pg::attend_row_kernel<__half, 128><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  else pg::attend_row_kernel<__half, 64><<<grid, pg::kRowThreads, 0, stream>>>(p);
-  return launched();
+  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_prefill<__nv_bfloat16, 128>(p, stream)
+                      : bf                      ? pg::launch_prefill<__nv_bfloat16, 64>(p, stream)
+                      : d.head_dim == 128       ? pg::launch_prefill<__half, 128>(p, stream)
+                                                : pg::launch_prefill<__half, 64>(p, stream);
+  return launched(e);
 }
 
 void mla_gqa_prefill_plan_destroy(mla_gqa_prefill_plan_t plan) { delete plan; }

@@ -81,6 +81,22 @@ __device__ __forceinline__ int32_t sequence_of(const CuSearch& s, const int32_t*
   return a < s.B ? a : -1;
 }
 
+// fp16 softmax weights: 2^-14 is the smallest normal value, so the weights of the
+// largest score are 2^8 instead of 1 and the maximum moves after 2^6; weights
+// then stay below 2^14 and are normal numbers down to 2^-22 of the largest.
+// bf16 has fp32's range: the maximum moves after 2^8.
+template <typename T> struct WeightScale { static constexpr float bias = 0.f, lazy = 8.f; };
+template <> struct WeightScale<__half> { static constexpr float bias = 8.f, lazy = 6.f; };
+
+// The tokens of sequence b; a length out of range counts as 0 (`tell`: record it).
+__device__ __forceinline__ int32_t checked_len(const GqaParams& p, int32_t b, bool tell) {
+  const int32_t L = p.seq_lens[b];
+  if (L >= 0 && (int64_t)L <= (int64_t)p.bt_stride * kPage) return L;
+  if (tell) record_error(p.status, MLA_ERR_BOUNDS);
+  return 0;
+}
+__device__ __forceinline__ int32_t pages_of(int32_t L) { return (L + kPage - 1) / kPage; }
+
 // ------------------------------------------------------------ tensor maps ----
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,

@@ -49,12 +49,6 @@ template <int kD> struct DecodeSmem {
   static_assert(2 * (alloc + 1024) <= 228 * 1024, "two workers share an SM");
 };
 
-// fp16 weights: 2^-14 is the smallest normal value, so the weights of the
-// largest score are 2^8 instead of 1 and the maximum moves after 2^6; weights
-// then stay below 2^14 and are normal numbers down to 2^-22 of the largest.
-template <typename T> struct WeightScale { static constexpr float bias = 0.f, lazy = 8.f; };
-template <> struct WeightScale<__half> { static constexpr float bias = 8.f, lazy = 6.f; };
-
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
@@ -78,14 +72,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-// The tokens of sequence b; a length out of range counts as 0 (`tell`: record it).
-__device__ __forceinline__ int32_t checked_len(const GqaParams& p, int32_t b, bool tell) {
-  const int32_t L = p.seq_lens[b];
-  if (L >= 0 && (int64_t)L <= (int64_t)p.bt_stride * kPage) return L;
-  if (tell) record_error(p.status, MLA_ERR_BOUNDS);
-  return 0;
-}
-__device__ __forceinline__ int32_t pages_of(int32_t L) { return (L + kPage - 1) / kPage; }
 // An item's places on the line.
 __device__ __forceinline__ int64_t line_of(int32_t pages) { return pages ? pages + kItemCost : 0; }
 
