@@ -46,6 +46,13 @@ template <typename T> constexpr uint32_t idesc16(int M, int N, int a_mn, int b_m
   return std::is_same<T, __half>::value ? d & ~((1u << 7) | (1u << 10)) : d;
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // A from tensor memory: two 16-bit values per column, B by descriptor.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   auto full = [&](int s) -> uint32_t { return base + S::bars + 8u * s; };
   auto empty = [&](int s) -> uint32_t { return base + S::bars + 8u * (kSlots + s); };
   auto q_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + i); };
@@ -217,9 +224,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     }
   } else if (warp == 1) {
     // ----------------------------------------------------------- MMA issuer --
-    if (lane == 0 && nk > 0) {
+    // The warp stays converged and one elected lane issues: descriptors and
+    // addresses are then uniform, and an MMA costs a few issue slots. (Issued
+    // by lane 0 of a diverged warp, the 32 MMAs of a step took 4270 cycles.)
+    if (nk > 0) {
       constexpr uint32_t idesc_s = idesc16<T>(128, 128, 0, 0), idesc_o = idesc16<T>(128, kD, 0, 1);
+      const bool leader = elect_one();
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        ok = ok && mbar_wait(bar, parity, p.wait_limit_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        tc_fence_after();
+      };
       auto scores = [&](int i, int s) {
+        if (!ok || !leader) return;
         const uint64_t a = smem_desc_sw128(base + S::q + i * S::tile_bytes, 16, 1024);
         const uint64_t k = smem_desc_sw128(base + S::ring + s * S::tile_bytes, 16, 1024);
 #pragma unroll
@@ -230,54 +247,51 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         tc_commit<1>(s_full(i));
       };
       auto values = [&](int i, int s, bool more) {
+        if (!ok || !leader) return;
         const uint64_t v = smem_desc_sw128(base + S::ring + s * S::tile_bytes, kTile * 128, 1024);
 #pragma unroll
         for (int x = 0; x < kTile / 16; ++x)
           mma_ts(tbase + kTmemO + kD * i, tbase + 128 * i + 8 * x, v + (uint64_t)(128 * x), idesc_o, more || x ? 1u : 0u);
       };
+      auto done = [&](uint32_t bar) {
+        if (ok && leader) tc_commit<1>(bar);
+      };
       uint32_t it = 0;                   // the next ring item
       auto arrived = [&]() {
-        ok = ok && mbar_wait(full(it % kSlots), (it / kSlots) & 1, p.wait_limit_ns);
-        tc_fence_after();
+        wait(full(it % kSlots), (it / kSlots) & 1);
         return (int)(it++ % kSlots);
       };
       const int s = arrived();
       // a tile that sees no key is waited for too: its copy lands before the block ends
-      ok = ok && mbar_wait(q_full(0), 0, p.wait_limit_ns);
-      if (ok && nk0 > 0) scores(0, s);
-      if (two_tiles) ok = ok && mbar_wait(q_full(1), 0, p.wait_limit_ns);
-      if (ok && nk1 > 0) scores(1, s);
-      if (ok) tc_commit<1>(empty(s));
+      wait(q_full(0), 0);
+      if (nk0 > 0) scores(0, s);
+      if (two_tiles) wait(q_full(1), 0);
+      if (nk1 > 0) scores(1, s);
+      done(empty(s));
       for (int j = 0; j < nk && ok; ++j) {
         const int vs = arrived();
         int ks = 0;
         if (j < nk0) {
-          ok = ok && mbar_wait(p_full(0), j & 1, p.wait_limit_ns);
-          if (!ok) break;
-          tc_fence_after();
+          wait(p_full(0), j & 1);
           values(0, vs, j > 0);
-          if (j + 1 == nk0) tc_commit<1>(o_full(0));
+          if (j + 1 == nk0) done(o_full(0));
         }
         if (j + 1 < nk) {
           ks = arrived();
-          if (!ok) break;
           if (j + 1 < nk0) scores(0, ks);
         }
         if (j < nk1) {
-          ok = ok && mbar_wait(p_full(1), j & 1, p.wait_limit_ns);
-          if (!ok) break;
-          tc_fence_after();
+          wait(p_full(1), j & 1);
           values(1, vs, j > 0);
-          if (j + 1 == nk1) tc_commit<1>(o_full(1));
+          if (j + 1 == nk1) done(o_full(1));
         }
-        if (!ok) break;
-        tc_commit<1>(empty(vs));
+        done(empty(vs));
         if (j + 1 < nk) {
           if (j + 1 < nk1) scores(1, ks);
-          tc_commit<1>(empty(ks));
+          done(empty(ks));
         }
       }
-      if (!ok) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
+      if (!ok && lane == 0) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
     }
     __syncwarp();
   } else if (warp >= 4) {
