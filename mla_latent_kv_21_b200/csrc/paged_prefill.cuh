@@ -27,6 +27,7 @@ namespace pg {
 
 constexpr int kPrefillThreads = 384;
 constexpr int kTile = 128;               // rows of a tile, keys of a step
+constexpr int kEarlyKeys = 64;           // keys whose weights are handed over early
 
 template <int kD> struct PrefillSmem {
   static constexpr uint32_t tile_bytes = kTile * kD * 2;         // a query tile; a step's keys or values
@@ -139,6 +140,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   auto s_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 2 + i); };
   auto p_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 4 + i); };
   auto o_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 6 + i); };
+  auto p_part = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 8 + i); };
   uint32_t* tslot = reinterpret_cast<uint32_t*>(gbase + S::misc);
 
   if (threadIdx.x == 0) {
@@ -146,7 +148,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(q_full(i), 1);
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 4);    // the four softmax warps of the tile
+      mbar_init(p_part(i), 4);    // the four softmax warps of the tile
+      mbar_init(p_full(i), 4);
       mbar_init(o_full(i), 1);
     }
     fence_mbarrier_init_cluster();
@@ -178,7 +181,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const uint32_t tbase = *tslot;
   constexpr uint32_t kTmemO = 256;       // S (and P) of tile i: columns [128 i, +128); O: [256 + d i, +d)
   bool ok = true;
+  // 384 x 168 registers at launch: 128 x 72 + 256 x 216
 
+  if (warp < 4) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 0) {
     // ------------------------------------------------------------ producer --
     const int32_t q0 = (int32_t)(c0 + t0);
@@ -246,16 +252,19 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
         tc_commit<1>(s_full(i));
       };
-      auto values = [&](int i, int s, bool more) {
+      auto values = [&](int i, int s, bool more, auto x0, auto x1) {
         if (!ok || !leader) return;
         const uint64_t v = smem_desc_sw128(base + S::ring + s * S::tile_bytes, kTile * 128, 1024);
 #pragma unroll
-        for (int x = 0; x < kTile / 16; ++x)
+        for (int x = x0; x < x1; ++x)
           mma_ts(tbase + kTmemO + kD * i, tbase + 128 * i + 8 * x, v + (uint64_t)(128 * x), idesc_o, more || x ? 1u : 0u);
       };
       auto done = [&](uint32_t bar) {
         if (ok && leader) tc_commit<1>(bar);
       };
+      constexpr std::integral_constant<int, 0> k0{};
+      constexpr std::integral_constant<int, kEarlyKeys / 16> kEarly{};
+      constexpr std::integral_constant<int, kTile / 16> kAll{};
       uint32_t it = 0;                   // the next ring item
       auto arrived = [&]() {
         wait(full(it % kSlots), (it / kSlots) & 1);
@@ -272,8 +281,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         const int vs = arrived();
         int ks = 0;
         if (j < nk0) {
+          wait(p_part(0), j & 1);
+          values(0, vs, j > 0, k0, kEarly);
           wait(p_full(0), j & 1);
-          values(0, vs, j > 0);
+          values(0, vs, j > 0, kEarly, kAll);
           if (j + 1 == nk0) done(o_full(0));
         }
         if (j + 1 < nk) {
@@ -281,8 +292,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           if (j + 1 < nk0) scores(0, ks);
         }
         if (j < nk1) {
+          wait(p_part(1), j & 1);
+          values(1, vs, j > 0, k0, kEarly);
           wait(p_full(1), j & 1);
-          values(1, vs, j > 0);
+          values(1, vs, j > 0, kEarly, kAll);
           if (j + 1 == nk1) done(o_full(1));
         }
         done(empty(vs));
@@ -294,7 +307,9 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       if (!ok && lane == 0) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
     }
     __syncwarp();
-  } else if (warp >= 4) {
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // -------------------------------------------------------------- softmax --
     const int tile = (warp - 4) >> 2;
     const int row = 32 * (warp & 3) + lane;
@@ -335,13 +350,13 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           }
         }
       }
-      float x0 = -INFINITY, x1 = -INFINITY;
+      float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (int c = 0; c < kTile; c += 4) {
-        x0 = max_three(x0, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
-        x1 = max_three(x1, __uint_as_float(r[c + 2]), __uint_as_float(r[c + 3]));
-      }
-      const float top = fmaxf(x0, x1) * p.scale_log2;
+      for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          x[e] = max_three(x[e], __uint_as_float(r[c + 2 * e]), __uint_as_float(r[c + 2 * e + 1]));
+      const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
       const bool move = top > m + WS::lazy;      // also a row's first visible key (m = -inf)
       const float mn = move ? top : m;
       if (__any_sync(0xffffffffu, move && l > 0.f)) {
@@ -359,6 +374,20 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         }
       }
       m = mn;
+      if ((j + 1) * kTile > L && (tile == 0 || j >= nk0)) {
+        // the cache's last step: values of slots without a token may hold
+        // anything, and 0 times NaN is not 0. The first tile to use them
+        // clears them before its weights are handed over.
+        const int s = (2 * j + 1) % kSlots;
+        wait(full(s), ((2 * j + 1) / kSlots) & 1);
+        if (ok)
+          for (int i = row; i < ((j + 1) * kTile - L) * (kD / 8); i += 128) {
+            const int x = kTile - 1 - i / (kD / 8), c = i % (kD / 8);
+            *reinterpret_cast<uint4*>(gbase + S::ring + s * S::tile_bytes + (c >> 3) * (kTile * 128) + x * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+        fence_proxy_async_smem();
+      }
       const float shift = m == -INFINITY ? 0.f : WS::bias - m;
       const uint64_t sc = two(p.scale_log2, p.scale_log2), sh = two(shift, shift);
       uint64_t sum0 = two(0.f, 0.f), sum1 = sum0;
@@ -376,23 +405,15 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
           w[e / 2 + 1] = Pack<T>::of(y2, y3);
         }
         tmem_st16(s_cols + c / 2, w);   // over scores that are in registers
+        if (c + 32 == kEarlyKeys) {
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_local(p_part(tile));
+        }
       }
       const float2 u0 = apart(sum0), u1 = apart(sum1);
       l += (u0.x + u0.y) + (u1.x + u1.y);
-      if ((j + 1) * kTile > L && (tile == 0 || j >= nk0)) {
-        // the cache's last step: values of slots without a token may hold
-        // anything, and 0 times NaN is not 0. The first tile to use them
-        // clears them before its weights are handed over.
-        const int s = (2 * j + 1) % kSlots;
-        wait(full(s), ((2 * j + 1) / kSlots) & 1);
-        if (ok)
-          for (int i = row; i < ((j + 1) * kTile - L) * (kD / 8); i += 128) {
-            const int x = kTile - 1 - i / (kD / 8), c = i % (kD / 8);
-            *reinterpret_cast<uint4*>(gbase + S::ring + s * S::tile_bytes + (c >> 3) * (kTile * 128) + x * 128 + (c & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-        fence_proxy_async_smem();
-      }
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
