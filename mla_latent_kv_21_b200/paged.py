@@ -10,7 +10,6 @@ per stream (or per captured graph) that may overlap with another.
 
 from __future__ import annotations
 
-import contextlib
 from typing import Optional, Sequence
 
 from . import _lib as L
@@ -60,10 +59,9 @@ class _Bound:
                 stream = torch.cuda.current_stream().cuda_stream
             return L.mla_decode_read_status(self.workspace.data_ptr(), stream)
 
-    def _enter(self, t, stream):
-        """(context that makes t's device current, stream handle), with the workspace in place."""
+    def _launch(self, dev: int, stream, call, *args) -> None:
+        """call(*args, workspace, workspace bytes, stream) with device `dev` current."""
         import torch
-        dev = t.device
         if self.workspace is None:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("allocate_workspace() before capturing: memory allocated under a capture belongs "
@@ -71,41 +69,40 @@ class _Bound:
             self.allocate_workspace(dev)
             if stream is not None:  # the allocation and its clearing are ordered on the current stream
                 torch.cuda.ExternalStream(stream, device=dev).wait_stream(torch.cuda.current_stream(dev))
-        elif self.workspace.device != dev:
-            raise ValueError(f"the workspace is on {self.workspace.device}, the tensors on {dev}")
+        elif self.workspace.get_device() != dev:
+            raise ValueError(f"the workspace is on {self.workspace.device}, the tensors on cuda:{dev}")
         if stream is None:
             stream = torch.cuda.current_stream(dev).cuda_stream
-        here = contextlib.nullcontext() if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        return here, stream
+        if dev == torch.cuda.current_device():
+            call(*args, self.workspace.data_ptr(), self.workspace_bytes, stream)
+        else:
+            with torch.cuda.device(dev):
+                call(*args, self.workspace.data_ptr(), self.workspace_bytes, stream)
 
 
-def _say(name, t, dtype, shape):
-    want = tuple("*" if e is None else e for e in shape)
-    return ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, needed: {dtype} {want}")
+def _shapes(args) -> None:
+    """(name, tensor, dtype, shape) of every argument (an extent of -1: any). The C ABI sees bare pointers, so a
+    mismatch is caught here."""
+    for name, t, dtype, shape in args:
+        got = t.shape
+        if t.dtype != dtype or (got != shape and (len(got) != len(shape) or
+                                                  any(n != e and e != -1 for n, e in zip(got, shape)))):
+            want = ", ".join("*" if e == -1 else str(e) for e in shape)
+            raise ValueError(f"{name}: {t.dtype} {tuple(got)}, needed: {dtype} ({want})")
 
 
-def _shape(name, t, dtype, shape):
-    """dtype and shape of one argument (None: any extent). The C ABI sees bare pointers, so a mismatch is caught here."""
-    got = t.shape
-    if t.dtype != dtype or len(got) != len(shape):
-        raise _say(name, t, dtype, shape)
-    for e, n in zip(shape, got):
-        if e is not None and e != n:
-            raise _say(name, t, dtype, shape)
-
-
-def _placed(dev, sources, dense) -> None:
-    """sources: views whose last dimension is contiguous; dense: contiguous tensors; all on one device."""
-    for name, t in dense:
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
-    for name, t in sources:
-        if not t.is_cuda or (t.numel() and t.stride(-1) != 1):
-            raise ValueError(f"{name} must be a CUDA tensor with a contiguous last dimension")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, other tensors on {dev}")
+def _placed(dev: int, sources, dense) -> None:
+    """sources: views whose last dimension is contiguous; dense: contiguous tensors; all on device `dev`."""
+    for name, t, _, _ in dense:
+        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA tensor")
+            raise ValueError(f"{name} is on {t.device}, other tensors on device {dev}")
+    for name, t, _, _ in sources:
+        if t.get_device() != dev or dev < 0 or (t.stride(-1) != 1 and t.numel()):
+            if not t.is_cuda or t.stride(-1) != 1:
+                raise ValueError(f"{name} must be a CUDA tensor with a contiguous last dimension")
+            raise ValueError(f"{name} is on {t.device}, other tensors on device {dev}")
 
 
 def _act(code):
@@ -129,45 +126,39 @@ class GqaAppend(_Bound):
         None: dims.q_len new tokens for every sequence."""
         import torch
         d, act, i32 = self.dims, self._dtype, torch.int32
-        T, Hq, Hk, hd = k.shape[0], d.num_q_heads, d.num_kv_heads, d.head_dim
-        B = seq_lens.shape[0]
-        _shape("k", k, act, (T, Hk, hd))
-        _shape("v", v, act, (T, Hk, hd))
-        _shape("k_pool", k_pool, act, (None, Hk, d.page_size, hd))
-        _shape("v_pool", v_pool, act, k_pool.shape)
-        _shape("block_table", block_table, i32, (B, None))
-        _shape("seq_lens", seq_lens, i32, (B,))
-        sources = [("k", k), ("v", v)]
-        dense = [("k_pool", k_pool), ("v_pool", v_pool), ("block_table", block_table), ("seq_lens", seq_lens)]
-        if not d.rope_dim:
-            rope_table = None
-        elif rope_table is None:
-            raise ValueError("rope_table is needed: the dims rotate")
-        else:
-            _shape("rope_table", rope_table, torch.float32, (None, d.rope_dim))
-            dense.append(("rope_table", rope_table))
-        if cu_seqlens is not None:
-            _shape("cu_seqlens", cu_seqlens, i32, (B + 1,))
-            dense.append(("cu_seqlens", cu_seqlens))
-        elif T != B * d.q_len:
-            raise ValueError(f"k: {T} tokens, needed without cu_seqlens: {B} x {d.q_len}")
+        Hq, Hk, hd, D = d.num_q_heads, d.num_kv_heads, d.head_dim, d.rope_dim
+        T, B, pool = k.shape[0], seq_lens.shape[0], (k_pool.shape[0], Hk, d.page_size, hd)
+        sources = [("k", k, act, (T, Hk, hd)), ("v", v, act, (T, Hk, hd))]
+        dense = [("k_pool", k_pool, act, pool), ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (B, -1)),
+                 ("seq_lens", seq_lens, i32, (B,))]
+        q_args, cu, table, positions = (None, 0, 0, None), None, None, 0
         if (q is None) != (q_out is None):
             raise ValueError("q and q_out come together")
+        if D and rope_table is None:
+            raise ValueError("rope_table is needed: the dims rotate")
+        if D:
+            dense.append(("rope_table", rope_table, torch.float32, (-1, D)))
+            table = rope_table.data_ptr()
+        if cu_seqlens is not None:
+            dense.append(("cu_seqlens", cu_seqlens, i32, (B + 1,)))
+            cu = cu_seqlens.data_ptr()
         if q is not None:
-            _shape("q", q, act, (T, Hq, hd))
-            _shape("q_out", q_out, act, (T, Hq, hd))
-            sources.append(("q", q))
-            dense.append(("q_out", q_out))
-        _placed(k.device, sources, dense)
-        args = L.mla_gqa_append_args_t(
-            k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-            *((None, 0, 0, None) if q is None else (q.data_ptr(), q.stride(0), q.stride(1), q_out.data_ptr())),
-            k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0], block_table.data_ptr(), block_table.shape[1], B,
-            seq_lens.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(), T,
-            None if rope_table is None else rope_table.data_ptr(), 0 if rope_table is None else rope_table.shape[0])
-        here, stream = self._enter(k, stream)
-        with here:
-            L.mla_gqa_append(d, args, self.workspace.data_ptr(), self.workspace_bytes, stream)
+            sources.append(("q", q, act, (T, Hq, hd)))
+            dense.append(("q_out", q_out, act, (T, Hq, hd)))
+        _shapes(sources)
+        _shapes(dense)
+        if cu is None and T != B * d.q_len:
+            raise ValueError(f"k: {T} tokens, needed without cu_seqlens: {B} x {d.q_len}")
+        dev = k.get_device()
+        _placed(dev, sources, dense)
+        if q is not None:
+            q_args = (q.data_ptr(), *q.stride()[:2], q_out.data_ptr())
+        if D:
+            positions = rope_table.shape[0]
+        args = L.mla_gqa_append_args_t(k.data_ptr(), *k.stride()[:2], v.data_ptr(), *v.stride()[:2], *q_args,
+                                       k_pool.data_ptr(), v_pool.data_ptr(), pool[0], block_table.data_ptr(),
+                                       block_table.shape[1], B, seq_lens.data_ptr(), cu, T, table, positions)
+        self._launch(dev, stream, L.mla_gqa_append, d, args)
 
 
 class LatentAppend(_Bound):
@@ -188,9 +179,8 @@ class LatentAppend(_Bound):
         d = self.dims
         if d.dtype == L.MLA_FP8_CACHE:
             raise ValueError("dims of the FP8 cache append with run_fp8")
-        _shape("kv_pool", kv_pool, self._dtype, (None, d.page_size, d.latent_rank + d.rope_dim))
-        self._run(ckv, k_rope, (("kv_pool", kv_pool),), block_table, seq_lens, rope_table, q_rope, q_rope_out, kv_rows,
-                  cu_seqlens, stream)
+        pools = [("kv_pool", kv_pool, self._dtype, (-1, d.page_size, d.latent_rank + d.rope_dim))]
+        self._run(ckv, k_rope, pools, block_table, seq_lens, rope_table, q_rope, q_rope_out, kv_rows, cu_seqlens, stream)
 
     def run_fp8(self, ckv, k_rope, kv_codes, kv_rope, kv_scale, block_table, seq_lens, rope_table, q_rope=None,
                 q_rope_out=None, kv_rows=None, cu_seqlens=None, stream: Optional[int] = None) -> None:
@@ -200,61 +190,48 @@ class LatentAppend(_Bound):
         d = self.dims
         if d.dtype != L.MLA_FP8_CACHE:
             raise ValueError("run_fp8 needs dims made with dtype 'fp8'")
-        _shape("kv_codes", kv_codes, torch.uint8, (None, d.page_size, d.latent_rank))
-        nb = kv_codes.shape[0]
-        _shape("kv_rope", kv_rope, torch.bfloat16, (nb, d.page_size, d.rope_dim))
-        _shape("kv_scale", kv_scale, torch.float32, (nb, d.page_size))
-        self._run(ckv, k_rope, (("kv_codes", kv_codes), ("kv_rope", kv_rope), ("kv_scale", kv_scale)), block_table,
-                  seq_lens, rope_table, q_rope, q_rope_out, kv_rows, cu_seqlens, stream)
+        nb, P = kv_codes.shape[0], d.page_size
+        pools = [("kv_codes", kv_codes, torch.uint8, (nb, P, d.latent_rank)),
+                 ("kv_rope", kv_rope, torch.bfloat16, (nb, P, d.rope_dim)), ("kv_scale", kv_scale, torch.float32, (nb, P))]
+        self._run(ckv, k_rope, pools, block_table, seq_lens, rope_table, q_rope, q_rope_out, kv_rows, cu_seqlens, stream)
 
     def _run(self, ckv, k_rope, pools, block_table, seq_lens, rope_table, q_rope, q_rope_out, kv_rows, cu_seqlens,
              stream):
         import torch
         d, act, i32 = self.dims, self._dtype, torch.int32
-        T, H, r, D = ckv.shape[0], d.num_heads, d.latent_rank, d.rope_dim
-        B = seq_lens.shape[0]
-        _shape("ckv", ckv, act, (T, r))
-        _shape("block_table", block_table, i32, (B, None))
-        _shape("seq_lens", seq_lens, i32, (B,))
-        sources = [("ckv", ckv)]
-        dense = [*pools, ("block_table", block_table), ("seq_lens", seq_lens)]
-        if D:
-            if k_rope is None or rope_table is None:
-                raise ValueError("k_rope and rope_table are needed: the dims rotate")
-            _shape("k_rope", k_rope, act, (T, D))
-            _shape("rope_table", rope_table, torch.float32, (None, D))
-            sources.append(("k_rope", k_rope))
-            dense.append(("rope_table", rope_table))
-        else:
-            k_rope = rope_table = None
+        H, r, D = d.num_heads, d.latent_rank, d.rope_dim
+        T, B = ckv.shape[0], seq_lens.shape[0]
+        sources = [("ckv", ckv, act, (T, r))]
+        dense = [*pools, ("block_table", block_table, i32, (B, -1)), ("seq_lens", seq_lens, i32, (B,))]
         if (q_rope is None) != (q_rope_out is None):
             raise ValueError("q_rope and q_rope_out come together")
+        if D and (k_rope is None or rope_table is None):
+            raise ValueError("k_rope and rope_table are needed: the dims rotate")
+        if D:
+            sources.append(("k_rope", k_rope, act, (T, D)))
+            dense.append(("rope_table", rope_table, torch.float32, (-1, D)))
         if q_rope is not None:
-            _shape("q_rope", q_rope, act, (T, H, D))
-            _shape("q_rope_out", q_rope_out, act, (T, H, D))
-            sources.append(("q_rope", q_rope))
-            dense.append(("q_rope_out", q_rope_out))
+            sources.append(("q_rope", q_rope, act, (T, H, D)))
+            dense.append(("q_rope_out", q_rope_out, act, (T, H, D)))
         if kv_rows is not None:
-            _shape("kv_rows", kv_rows, act, (T, r + D))
-            dense.append(("kv_rows", kv_rows))
+            dense.append(("kv_rows", kv_rows, act, (T, r + D)))
         if cu_seqlens is not None:
-            _shape("cu_seqlens", cu_seqlens, i32, (B + 1,))
-            dense.append(("cu_seqlens", cu_seqlens))
-        elif T != B * d.q_len:
+            dense.append(("cu_seqlens", cu_seqlens, i32, (B + 1,)))
+        _shapes(sources)
+        _shapes(dense)
+        if cu_seqlens is None and T != B * d.q_len:
             raise ValueError(f"ckv: {T} tokens, needed without cu_seqlens: {B} x {d.q_len}")
-        _placed(ckv.device, sources, dense)
-        pool, rope, scale = [t for _, t in pools] + [None] * (3 - len(pools))
+        dev = ckv.get_device()
+        _placed(dev, sources, dense)
         at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        args = L.mla_latent_append_args_t(
-            ckv.data_ptr(), ckv.stride(0), at(k_rope), 0 if k_rope is None else k_rope.stride(0),
-            *((None, 0, 0, None) if q_rope is None else (q_rope.data_ptr(), q_rope.stride(0), q_rope.stride(1),
-                                                         q_rope_out.data_ptr())),
-            pool.data_ptr(), at(rope), at(scale), at(kv_rows), pool.shape[0], block_table.data_ptr(),
-            block_table.shape[1], B, seq_lens.data_ptr(), at(cu_seqlens), T, at(rope_table),
-            0 if rope_table is None else rope_table.shape[0])
-        here, stream = self._enter(ckv, stream)
-        with here:
-            L.mla_latent_append(d, self.style, args, self.workspace.data_ptr(), self.workspace_bytes, stream)
+        key = (k_rope.data_ptr(), k_rope.stride(0)) if D else (None, 0)
+        q_args = (None, 0, 0, None) if q_rope is None else (q_rope.data_ptr(), *q_rope.stride()[:2], q_rope_out.data_ptr())
+        out = [t.data_ptr() for _, t, _, _ in pools] + [None] * (3 - len(pools))
+        table = (rope_table.data_ptr(), rope_table.shape[0]) if D else (None, 0)
+        args = L.mla_latent_append_args_t(ckv.data_ptr(), ckv.stride(0), *key, *q_args, *out, at(kv_rows),
+                                          pools[0][1].shape[0], block_table.data_ptr(), block_table.shape[1], B,
+                                          seq_lens.data_ptr(), at(cu_seqlens), T, *table)
+        self._launch(dev, stream, L.mla_latent_append, d, self.style, args)
 
 
 class _GqaPlan(_Bound):
@@ -263,17 +240,19 @@ class _GqaPlan(_Bound):
     handle = None
     _destroy = None
 
-    def _attend(self, q, out, k_pool, v_pool, shape, more):
+    def _attend(self, run, stream, shape, q, out, k_pool, v_pool, block_table, lengths):
+        """The checks and the call; lengths: the int32 tensors by (name, tensor, extent), in the call's order."""
         import torch
-        d, act = self.dims, self._dtype
-        _shape("q", q, act, shape)
-        _shape("out", out, act, shape)
-        _shape("k_pool", k_pool, act, (None, d.num_kv_heads, d.page_size, d.head_dim))
-        _shape("v_pool", v_pool, act, k_pool.shape)
-        for name, t, extent in more:
-            _shape(name, t, torch.int32, extent)
-        _placed(q.device, (), (("q", q), ("out", out), ("k_pool", k_pool), ("v_pool", v_pool),
-                               *[(name, t) for name, t, _ in more]))
+        d, act, i32 = self.dims, self._dtype, torch.int32
+        pool = (k_pool.shape[0], d.num_kv_heads, d.page_size, d.head_dim)
+        args = [("q", q, act, shape), ("out", out, act, shape), ("k_pool", k_pool, act, pool),
+                ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (self.batch, -1)),
+                *[(name, t, i32, (n,)) for name, t, n in lengths]]
+        _shapes(args)
+        dev = q.get_device()
+        _placed(dev, (), args)
+        self._launch(dev, stream, run, self.handle, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), pool[0],
+                     block_table.data_ptr(), block_table.shape[1], *[t.data_ptr() for _, t, _ in lengths], out.data_ptr())
 
     def close(self) -> None:
         if self.handle:
@@ -302,14 +281,9 @@ class GqaDecodePlan(_GqaPlan):
     def run(self, q, k_pool, v_pool, block_table, seq_lens, out, stream: Optional[int] = None) -> None:
         """q, out [B, Lq, Hq, d]; k_pool, v_pool [num_blocks, Hk, 64, d]; block_table int32 [B, *]; seq_lens int32 [B],
         the Lq queries' tokens counted: contiguous CUDA tensors."""
-        d, B = self.dims, self.batch
-        self._attend(q, out, k_pool, v_pool, (B, d.q_len, d.num_q_heads, d.head_dim),
-                     (("block_table", block_table, (B, None)), ("seq_lens", seq_lens, (B,))))
-        here, stream = self._enter(q, stream)
-        with here:
-            L.mla_gqa_decode_run(self.handle, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0],
-                                 block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(), out.data_ptr(),
-                                 self.workspace.data_ptr(), self.workspace_bytes, stream)
+        d = self.dims
+        self._attend(L.mla_gqa_decode_run, stream, (self.batch, d.q_len, d.num_q_heads, d.head_dim), q, out, k_pool, v_pool,
+                     block_table, (("seq_lens", seq_lens, self.batch),))
 
 
 class GqaPrefillPlan(_GqaPlan):
@@ -321,20 +295,13 @@ class GqaPrefillPlan(_GqaPlan):
     def __init__(self, dims: L.mla_gqa_dims_t, new_tokens_host: Sequence[int]):
         self.dims = dims
         self.new_tokens = [int(x) for x in new_tokens_host]
-        self.tokens = sum(self.new_tokens)
+        self.batch, self.tokens = len(self.new_tokens), sum(self.new_tokens)
         self._dtype = _act(dims.dtype)
         self.handle, self.workspace_bytes = L.mla_gqa_prefill_plan(dims, self.new_tokens)
 
     def run(self, q, k_pool, v_pool, block_table, cu_seqlens, seq_lens, out, stream: Optional[int] = None) -> None:
         """q, out [T, Hq, d] packed; k_pool, v_pool [num_blocks, Hk, 64, d]; block_table int32 [B, *]; cu_seqlens int32
         [B + 1], the prefix sums of the new tokens; seq_lens int32 [B], all tokens: contiguous CUDA tensors."""
-        d, B = self.dims, len(self.new_tokens)
-        self._attend(q, out, k_pool, v_pool, (self.tokens, d.num_q_heads, d.head_dim),
-                     (("block_table", block_table, (B, None)), ("cu_seqlens", cu_seqlens, (B + 1,)),
-                      ("seq_lens", seq_lens, (B,))))
-        here, stream = self._enter(q, stream)
-        with here:
-            L.mla_gqa_prefill_run(self.handle, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), k_pool.shape[0],
-                                  block_table.data_ptr(), block_table.shape[1], cu_seqlens.data_ptr(),
-                                  seq_lens.data_ptr(), out.data_ptr(), self.workspace.data_ptr(), self.workspace_bytes,
-                                  stream)
+        d = self.dims
+        self._attend(L.mla_gqa_prefill_run, stream, (self.tokens, d.num_q_heads, d.head_dim), q, out, k_pool, v_pool,
+                     block_table, (("cu_seqlens", cu_seqlens, self.batch + 1), ("seq_lens", seq_lens, self.batch)))
