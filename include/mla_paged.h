@@ -21,8 +21,8 @@
  *   tokens of the call, which are the newest of the cache.
  * Packed tokens: cu_seqlens int32 [B + 1] (device), sequence b owns rows
  * [cu[b], cu[b+1]) of the packed tensors; n_b = cu[b+1] - cu[b] of its L_b
- * tokens are new. Rows at or behind cu[B] belong to no sequence: they are not
- * read and their outputs are left as they were.
+ * tokens are new. Rows at or behind cu[B] belong to no sequence: nothing is made
+ * of them and their outputs are left as they were.
  *
  * Slots of a page past L_b are never used, whatever they hold (NaN included).
  * Keys and values of a sequence's own tokens must be finite.

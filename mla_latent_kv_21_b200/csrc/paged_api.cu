@@ -49,6 +49,11 @@ mla_status_t launched(cudaError_t e = cudaSuccess) {
   return e == cudaSuccess && last == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
+// Heads that a thread of an append walks, over token blocks x head blocks of 128
+// threads: 16 where that still fills the machine (its angles are then loaded
+// once for 16 heads), else 4 (one batch of loads).
+int heads_per_block(int64_t token_blocks, int H) { return token_blocks * ((H + 15) / 16) >= 1184 ? 16 : 4; }
+
 // Rows of the cache and of the batch: tensor-map and grid coordinates are 32-bit.
 bool fits32(int64_t rows) { return rows < (int64_t(1) << 31); }
 
@@ -100,9 +105,7 @@ mla_status_t mla_gqa_append(const mla_gqa_dims_t* dims, const mla_gqa_append_arg
   p.D = d.rope_dim;
   const int H = (a.q ? p.Hq : 0) + 2 * p.Hk, tokens = pg::kAppendThreads / (p.d / 16);
   const int64_t gx = (p.T + tokens - 1) / tokens;
-  // a thread's heads: 16 where that still fills the machine, else 4 (one batch
-  // of loads)
-  p.heads_per_cta = gx * ((H + 15) / 16) >= 1184 ? 16 : 4;
+  p.heads_per_cta = heads_per_block(gx, H);
   const dim3 grid((unsigned)gx, (unsigned)((H + p.heads_per_cta - 1) / p.heads_per_cta));
   const int half = d.rope_style == MLA_ROPE_HALF;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
@@ -167,13 +170,24 @@ mla_status_t mla_latent_append(const mla_dims_t* dims, int32_t rope_style, const
   p.r = d.latent_rank;
   const int half = rope_style == MLA_ROPE_HALF;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const dim3 grid((unsigned)p.T);
-  const int n = pg::kLatentThreads;
-  if (fp8) pg::latent_append_kernel<__nv_bfloat16, true><<<grid, n, 0, stream>>>(p, half);
-  else if (wide && d.dtype == MLA_BF16) pg::latent_append_kernel<__nv_bfloat16, false><<<grid, n, 0, stream>>>(p, half);
-  else if (wide) pg::latent_append_kernel<float, false><<<grid, n, 0, stream>>>(p, half);
-  else if (d.dtype == MLA_BF16) pg::latent_append_narrow_kernel<__nv_bfloat16><<<grid, n, 0, stream>>>(p, half);
-  else pg::latent_append_narrow_kernel<float><<<grid, n, 0, stream>>>(p, half);
+  if (wide) {
+    int64_t blocks = (p.T + 3) / 4;
+    if (a.q_rope) {
+      const int tokens = pg::kAppendThreads / (p.D / (2 * V));
+      const int64_t gx = (p.T + tokens - 1) / tokens;
+      p.heads_per_cta = heads_per_block(gx, p.Hq);
+      blocks += gx * ((p.Hq + p.heads_per_cta - 1) / p.heads_per_cta);
+    }
+    if (!fits32(blocks)) return MLA_ERR_UNSUPPORTED;
+    const unsigned n = (unsigned)blocks;
+    if (fp8) pg::latent_append_kernel<__nv_bfloat16, true><<<n, pg::kAppendThreads, 0, stream>>>(p, half);
+    else if (V == 8) pg::latent_append_kernel<__nv_bfloat16, false><<<n, pg::kAppendThreads, 0, stream>>>(p, half);
+    else pg::latent_append_kernel<float, false><<<n, pg::kAppendThreads, 0, stream>>>(p, half);
+  } else if (V == 8) {
+    pg::latent_append_narrow_kernel<__nv_bfloat16><<<(unsigned)p.T, pg::kNarrowThreads, 0, stream>>>(p, half);
+  } else {
+    pg::latent_append_narrow_kernel<float><<<(unsigned)p.T, pg::kNarrowThreads, 0, stream>>>(p, half);
+  }
   return launched();
 }
 

@@ -53,7 +53,7 @@ __device__ __forceinline__ Place place_of(const AppendParams& p, const CuSearch&
   if (p.cu) {
     b = sequence_of(cs, cu_shared, (int32_t)t);
     if (b < 0) return r;
-    const int64_t c0 = p.cu[b], c1 = p.cu[b + 1];
+    const int64_t c0 = cs.step == 1 ? cu_shared[b] : p.cu[b], c1 = cs.step == 1 ? cu_shared[b + 1] : p.cu[b + 1];
     if (t >= c1) return r;          // prefix sums that do not rise own no such token
     n = c1 - c0;
     i = t - c0;
@@ -112,26 +112,23 @@ template <> struct Vec<float> {
 // A unit's place in a head of which D elements rotate, and its angles.
 template <typename T> struct Unit {
   static constexpr int V = Vec<T>::n;
-  int at0, at1;            // element offsets of its two vectors
+  int u, at0, at1;         // its number; element offsets of its two vectors
   bool turn, half;
   float c[V], s[V];
 
-  __device__ __forceinline__ Unit(int u, int D, bool half_style, const float* row) {
-    half = half_style;
+  __device__ __forceinline__ Unit(int u_, int D, bool half_style) : u(u_), half(half_style) {
     turn = u < D / (2 * V);
     at0 = turn && half ? u * V : 2 * u * V;
     at1 = at0 + (turn && half ? D / 2 : V);
-    if (turn) {
+  }
+  __device__ __forceinline__ void angles(const float* row, int D) {
+    if (!turn) return;
 #pragma unroll
-      for (int i = 0; i < V; i += 4) {
-        const float4 a = *reinterpret_cast<const float4*>(row + u * V + i);
-        const float4 b = *reinterpret_cast<const float4*>(row + D / 2 + u * V + i);
-        c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
-        s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) { c[i] = 1.f; s[i] = 0.f; }
+    for (int i = 0; i < V; i += 4) {
+      const float4 a = *reinterpret_cast<const float4*>(row + u * V + i);
+      const float4 b = *reinterpret_cast<const float4*>(row + D / 2 + u * V + i);
+      c[i] = a.x; c[i + 1] = a.y; c[i + 2] = a.z; c[i + 3] = a.w;
+      s[i] = b.x; s[i + 1] = b.y; s[i + 2] = b.z; s[i + 3] = b.w;
     }
   }
   // x0, x1: the values of the two vectors
@@ -155,11 +152,58 @@ template <typename T> struct Unit {
   }
 };
 
-// ----------------------------------------------------- grouped-head cache ----
-// Block (x, y): 128 threads = 128 / (d / 16) tokens x d / 16 units, heads
-// [y * heads_per_cta, ..) of the list q heads, k heads, v heads.
+// One thread's unit of the heads h0 to h1 - 1 of one token, four heads' loads
+// at a time and the next four under way while a batch is turned and stored.
+// place(): where the token goes and its angles, false if it goes nowhere; it is
+// called with the first loads in flight, since its chain of dependent reads
+// (prefix sums, length, block, table row) is as long as theirs.
+template <typename T, typename Src, typename Place, typename Dst>
+__device__ __forceinline__ void walk_heads(Unit<T>& unit, int h0, int h1, int turned, Src src, Place place, Dst dst) {
+  uint4 a[4], b[4];
+  auto load = [&](int hb) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (hb + j < h1) {
+        const T* x = src(hb + j);
+        a[j] = *reinterpret_cast<const uint4*>(x + unit.at0);
+        b[j] = *reinterpret_cast<const uint4*>(x + unit.at1);
+      }
+  };
+  load(h0);
+  if (!place()) return;
+  for (int hb = h0; hb < h1; hb += 4) {
+    uint4 x[4], y[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[j] = a[j];
+      y[j] = b[j];
+    }
+    if (hb + 4 < h1) load(hb + 4);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int h = hb + j;
+      if (h < h1) {
+        if (unit.turn && h < turned) {
+          float x0[Unit<T>::V], x1[Unit<T>::V];
+          Vec<T>::to(x[j], x0);
+          Vec<T>::to(y[j], x1);
+          unit.rotate(x0, x1);
+          x[j] = Vec<T>::of(x0);
+          y[j] = Vec<T>::of(x1);
+        }
+        T* z = dst(h);
+        *reinterpret_cast<uint4*>(z + unit.at0) = x[j];
+        *reinterpret_cast<uint4*>(z + unit.at1) = y[j];
+      }
+    }
+  }
+}
+
 constexpr int kAppendThreads = 128;
 
+// ----------------------------------------------------- grouped-head cache ----
+// Block (x, y): 128 / (d / 16) tokens x d / 16 units, heads [y * heads_per_cta,
+// ..) of the list q heads, k heads, v heads.
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) gqa_append_kernel(AppendParams p, int half_style) {
   __shared__ int32_t cu_shared[kCuShared + 1];
@@ -169,58 +213,34 @@ __global__ void __launch_bounds__(kAppendThreads) gqa_append_kernel(AppendParams
     __syncthreads();
   }
   const int units = p.d / 16;
-  const int u = threadIdx.x % units;
   const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / units) + threadIdx.x / units;
   if (t >= p.T) return;
-  const Place at = place_of(p, cs, cu_shared, t, u == 0 && blockIdx.y == 0);
-  if (at.pos < 0) return;
-  const Unit<T> unit(u, p.D, half_style != 0, p.table + at.pos * p.D);
+  Unit<T> unit(threadIdx.x % units, p.D, half_style != 0);
   const int nq = p.q ? p.Hq : 0, H = nq + 2 * p.Hk;
   const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(H, h0 + p.heads_per_cta);
-  for (int hb = h0; hb < h1; hb += 4) {
-    uint4 a[4], b[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int h = hb + j;
-      if (h < h1) {
-        const T* src = h < nq ? static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs
-                     : h < nq + p.Hk ? static_cast<const T*>(p.k) + t * p.k_ts + (h - nq) * p.k_hs
-                                     : static_cast<const T*>(p.v) + t * p.v_ts + (h - nq - p.Hk) * p.v_hs;
-        // a value head is copied: its unit's vectors are the same two
-        a[j] = *reinterpret_cast<const uint4*>(src + unit.at0);
-        b[j] = *reinterpret_cast<const uint4*>(src + unit.at1);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int h = hb + j;
-      if (h < h1) {
-        T* dst;
-        if (h < nq) {
-          dst = static_cast<T*>(p.q_out) + (t * p.Hq + h) * p.d;
-        } else {
-          const bool is_k = h < nq + p.Hk;
-          const int hk = h - nq - (is_k ? 0 : p.Hk);
-          dst = static_cast<T*>(is_k ? p.k_pool : p.v_pool) +
-                ((at.block * p.Hk + hk) * kPage + at.slot) * p.d;
-        }
-        if (unit.turn && h < nq + p.Hk) {
-          float x0[8], x1[8];
-          Vec<T>::to(a[j], x0);
-          Vec<T>::to(b[j], x1);
-          unit.rotate(x0, x1);
-          a[j] = Vec<T>::of(x0);
-          b[j] = Vec<T>::of(x1);
-        }
-        *reinterpret_cast<uint4*>(dst + unit.at0) = a[j];
-        *reinterpret_cast<uint4*>(dst + unit.at1) = b[j];
-      }
-    }
-  }
+  Place at;
+  walk_heads<T>(
+      unit, h0, h1, nq + p.Hk,
+      [&](int h) {
+        return h < nq ? static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs
+             : h < nq + p.Hk ? static_cast<const T*>(p.k) + t * p.k_ts + (h - nq) * p.k_hs
+                             : static_cast<const T*>(p.v) + t * p.v_ts + (h - nq - p.Hk) * p.v_hs;
+      },
+      [&]() {
+        at = place_of(p, cs, cu_shared, t, unit.u == 0 && blockIdx.y == 0);
+        if (at.pos >= 0) unit.angles(p.table + at.pos * p.D, p.D);
+        return at.pos >= 0;
+      },
+      [&](int h) {
+        if (h < nq) return static_cast<T*>(p.q_out) + (t * p.Hq + h) * p.d;
+        const bool is_k = h < nq + p.Hk;
+        const int hk = h - nq - (is_k ? 0 : p.Hk);
+        return static_cast<T*>(is_k ? p.k_pool : p.v_pool) + ((at.block * p.Hk + hk) * kPage + at.slot) * p.d;
+      });
 }
 
 // ----------------------------------------------------------- latent cache ----
-constexpr int kLatentThreads = 256;
+constexpr int kNarrowThreads = 256;
 
 // One pair of the rotated part, element by element (any D, any alignment).
 template <typename T>
@@ -235,7 +255,7 @@ __device__ __forceinline__ void turn_pair(const T* src, int i, int D, bool half,
 
 // Narrow path (bf16 and fp32 caches): one block per token, element by element.
 template <typename T>
-__global__ void __launch_bounds__(kLatentThreads) latent_append_narrow_kernel(AppendParams p, int half_style) {
+__global__ void __launch_bounds__(kNarrowThreads) latent_append_narrow_kernel(AppendParams p, int half_style) {
   __shared__ int32_t cu_shared[kCuShared + 1];
   CuSearch cs{};
   if (p.cu) {
@@ -251,13 +271,13 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_narrow_kernel(Ap
   const T* kr = static_cast<const T*>(p.v) + t * p.v_ts;
   T* dst = static_cast<T*>(p.k_pool) + (at.block * kPage + at.slot) * (int64_t)width;
   T* rows = p.kv_rows ? static_cast<T*>(p.kv_rows) + t * width : nullptr;
-  for (int i = threadIdx.x; i < p.r; i += kLatentThreads) {
+  for (int i = threadIdx.x; i < p.r; i += kNarrowThreads) {
     dst[i] = c[i];
     if (rows) rows[i] = c[i];
   }
   float xa, xb;
   int ia, ib;
-  for (int i = threadIdx.x; i < p.D / 2; i += kLatentThreads) {
+  for (int i = threadIdx.x; i < p.D / 2; i += kNarrowThreads) {
     turn_pair(kr, i, p.D, half_style != 0, row, xa, xb, ia, ib);
     dst[p.r + ia] = from_float<T>(xa);
     dst[p.r + ib] = from_float<T>(xb);
@@ -267,7 +287,7 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_narrow_kernel(Ap
     }
   }
   if (!p.q) return;
-  for (int e = threadIdx.x; e < p.Hq * (p.D / 2); e += kLatentThreads) {
+  for (int e = threadIdx.x; e < p.Hq * (p.D / 2); e += kNarrowThreads) {
     const int h = e / (p.D / 2), i = e % (p.D / 2);
     turn_pair(static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs, i, p.D, half_style != 0, row, xa, xb, ia, ib);
     T* qo = static_cast<T*>(p.q_out) + (t * p.Hq + h) * (int64_t)p.D;
@@ -276,11 +296,11 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_narrow_kernel(Ap
   }
 }
 
-// Wide path: one block per token. Warp 0 writes the latent row, all threads
-// walk the query heads' units (D / (2 V) units per head, the same unit for a
-// thread every time, so its angles are loaded once).
+// Wide path. The first blocks write the latent rows, a warp per token; the
+// others turn the query heads as the grouped-head append does, 128 / (D / 2 V)
+// tokens and heads_per_cta heads to a block.
 template <typename T, bool kFp8>
-__global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(AppendParams p, int half_style) {
+__global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendParams p, int half_style) {
   using VT = Vec<T>;
   constexpr int V = VT::n;
   __shared__ int32_t cu_shared[kCuShared + 1];
@@ -289,92 +309,92 @@ __global__ void __launch_bounds__(kLatentThreads) latent_append_kernel(AppendPar
     cs = stage_cu(p.cu, p.B, cu_shared);
     __syncthreads();
   }
-  const int64_t t = blockIdx.x;
-  const Place at = place_of(p, cs, cu_shared, t, threadIdx.x == 0);
+  const int64_t row_blocks = (p.T + 3) / 4;
+  if (blockIdx.x >= row_blocks) {
+    const int units = p.D / (2 * V), tokens = kAppendThreads / units;
+    const int64_t token_blocks = (p.T + tokens - 1) / tokens, i = blockIdx.x - row_blocks;
+    const int64_t t = i % token_blocks * tokens + threadIdx.x / units;
+    if (t >= p.T || (int)threadIdx.x >= tokens * units) return;
+    Unit<T> unit(threadIdx.x % units, p.D, half_style != 0);
+    const int h0 = (int)(i / token_blocks) * p.heads_per_cta, h1 = min(p.Hq, h0 + p.heads_per_cta);
+    walk_heads<T>(
+        unit, h0, h1, h1, [&](int h) { return static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs; },
+        [&]() {
+          const Place at = place_of(p, cs, cu_shared, t, false);   // told by the latent row's warp
+          if (at.pos >= 0) unit.angles(p.table + at.pos * p.D, p.D);
+          return at.pos >= 0;
+        },
+        [&](int h) { return static_cast<T*>(p.q_out) + (t * p.Hq + h) * (int64_t)p.D; });
+    return;
+  }
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const int width = p.r + p.D, lane = threadIdx.x & 31;
+  const T* c = static_cast<const T*>(p.k) + t * p.k_ts;
+  const T* kr = static_cast<const T*>(p.v) + t * p.v_ts;
+  // the latent: up to 512 elements, 16 per lane (FP8: 16 neighbours; else every 32nd vector)
+  constexpr int N = 16 / V;
+  uint4 v[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int e = kFp8 ? 16 * lane + V * i : V * (lane + 32 * i);
+    if (e < p.r) v[i] = *reinterpret_cast<const uint4*>(c + e);
+  }
+  const Place at = place_of(p, cs, cu_shared, t, lane == 0);
   if (at.pos < 0) return;
   const float* row = p.table + at.pos * p.D;
   const int64_t cell = at.block * kPage + at.slot;
-  const int width = p.r + p.D, lane = threadIdx.x;
-  if (threadIdx.x < 32) {
-    const T* c = static_cast<const T*>(p.k) + t * p.k_ts;
-    const T* kr = static_cast<const T*>(p.v) + t * p.v_ts;
-    T* rows = p.kv_rows ? static_cast<T*>(p.kv_rows) + t * width : nullptr;
-    float scale = 1.f;
-    if constexpr (kFp8) {
-      // r = 512: 16 latent elements per lane
-      const uint4 v0 = *reinterpret_cast<const uint4*>(c + 16 * lane);
-      const uint4 v1 = *reinterpret_cast<const uint4*>(c + 16 * lane + 8);
-      if (rows) {
-        *reinterpret_cast<uint4*>(rows + 16 * lane) = v0;
-        *reinterpret_cast<uint4*>(rows + 16 * lane + 8) = v1;
-      }
-      float x0[8], x1[8], top = 0.f;
-      VT::to(v0, x0);
-      VT::to(v1, x1);
+  T* rows = p.kv_rows ? static_cast<T*>(p.kv_rows) + t * width : nullptr;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fmaxf(fabsf(x0[i]), fabsf(x1[i])));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      // correctly rounded divisions: the scale and the codes are those of the
-      // definition, bit for bit. The floor keeps s a normal number and
-      // k_rope / s inside bf16's range for a latent row of zeros.
-      scale = fmaxf(__fdiv_rn(top, 448.f), 5.421010862427522e-20f);   // 2^-64
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        w[i] = ptx::cvt_e4m3x2(__fdiv_rn(x0[4 * i], scale), __fdiv_rn(x0[4 * i + 1], scale)) |
-               ptx::cvt_e4m3x2(__fdiv_rn(x0[4 * i + 2], scale), __fdiv_rn(x0[4 * i + 3], scale)) << 16;
-        w[2 + i] = ptx::cvt_e4m3x2(__fdiv_rn(x1[4 * i], scale), __fdiv_rn(x1[4 * i + 1], scale)) |
-                   ptx::cvt_e4m3x2(__fdiv_rn(x1[4 * i + 2], scale), __fdiv_rn(x1[4 * i + 3], scale)) << 16;
-      }
-      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.k_pool) + cell * p.r + 16 * lane) =
-          make_uint4(w[0], w[1], w[2], w[3]);
-      if (lane == 0) p.kv_scale[cell] = scale;
-    } else {
-      T* dst = static_cast<T*>(p.k_pool) + cell * width;
-      for (int i = V * lane; i < p.r; i += 32 * V) {
-        const uint4 v = *reinterpret_cast<const uint4*>(c + i);
-        *reinterpret_cast<uint4*>(dst + i) = v;
-        if (rows) *reinterpret_cast<uint4*>(rows + i) = v;
-      }
-    }
-    for (int u = lane; u < p.D / (2 * V); u += 32) {
-      const Unit<T> unit(u, p.D, half_style != 0, row);
-      float x0[V], x1[V];
-      VT::to(*reinterpret_cast<const uint4*>(kr + unit.at0), x0);
-      VT::to(*reinterpret_cast<const uint4*>(kr + unit.at1), x1);
-      unit.rotate(x0, x1);
-      if (rows) {
-        *reinterpret_cast<uint4*>(rows + p.r + unit.at0) = VT::of(x0);
-        *reinterpret_cast<uint4*>(rows + p.r + unit.at1) = VT::of(x1);
-      }
-      T* dst;
-      if constexpr (kFp8) {
-        dst = static_cast<T*>(p.v_pool) + cell * p.D;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          x0[i] = __fdiv_rn(x0[i], scale);
-          x1[i] = __fdiv_rn(x1[i], scale);
-        }
-      } else {
-        dst = static_cast<T*>(p.k_pool) + cell * width + p.r;
-      }
-      *reinterpret_cast<uint4*>(dst + unit.at0) = VT::of(x0);
-      *reinterpret_cast<uint4*>(dst + unit.at1) = VT::of(x1);
-    }
+  for (int i = 0; i < N; ++i) {
+    const int e = kFp8 ? 16 * lane + V * i : V * (lane + 32 * i);
+    if (e >= p.r) continue;
+    if (rows) *reinterpret_cast<uint4*>(rows + e) = v[i];
+    if constexpr (!kFp8) *reinterpret_cast<uint4*>(static_cast<T*>(p.k_pool) + cell * width + e) = v[i];
   }
-  if (!p.q) return;   // the host refuses queries without a rotated part
-  const int units = p.D / (2 * V);
-  const int tpu = kLatentThreads / units;            // heads in flight
-  if ((int)threadIdx.x >= tpu * units) return;
-  const Unit<T> unit(threadIdx.x % units, p.D, half_style != 0, row);
-  for (int h = threadIdx.x / units; h < p.Hq; h += tpu) {
-    const T* src = static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs;
-    T* dst = static_cast<T*>(p.q_out) + (t * p.Hq + h) * (int64_t)p.D;
+  float scale = 1.f;
+  if constexpr (kFp8) {
+    float x[16], top = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) VT::to(v[i], *reinterpret_cast<float(*)[V]>(x + V * i));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // correctly rounded divisions: the scale and the codes are those of the
+    // definition, bit for bit. The floor keeps s a normal number and
+    // k_rope / s inside bf16's range for a latent row of zeros.
+    scale = fmaxf(__fdiv_rn(top, 448.f), 5.421010862427522e-20f);   // 2^-64
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      w[i] = ptx::cvt_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
+             ptx::cvt_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16;
+    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.k_pool) + cell * p.r + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane == 0) p.kv_scale[cell] = scale;
+  }
+  for (int u = lane; u < p.D / (2 * V); u += 32) {
+    Unit<T> unit(u, p.D, half_style != 0);
+    unit.angles(row, p.D);
     float x0[V], x1[V];
-    VT::to(*reinterpret_cast<const uint4*>(src + unit.at0), x0);
-    VT::to(*reinterpret_cast<const uint4*>(src + unit.at1), x1);
+    VT::to(*reinterpret_cast<const uint4*>(kr + unit.at0), x0);
+    VT::to(*reinterpret_cast<const uint4*>(kr + unit.at1), x1);
     unit.rotate(x0, x1);
+    if (rows) {
+      *reinterpret_cast<uint4*>(rows + p.r + unit.at0) = VT::of(x0);
+      *reinterpret_cast<uint4*>(rows + p.r + unit.at1) = VT::of(x1);
+    }
+    T* dst;
+    if constexpr (kFp8) {
+      dst = static_cast<T*>(p.v_pool) + cell * p.D;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        x0[i] = __fdiv_rn(x0[i], scale);
+        x1[i] = __fdiv_rn(x1[i], scale);
+      }
+    } else {
+      dst = static_cast<T*>(p.k_pool) + cell * width + p.r;
+    }
     *reinterpret_cast<uint4*>(dst + unit.at0) = VT::of(x0);
     *reinterpret_cast<uint4*>(dst + unit.at1) = VT::of(x1);
   }

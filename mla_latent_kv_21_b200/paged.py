@@ -39,6 +39,7 @@ class _Bound:
 
     workspace = None
     workspace_bytes = 1024
+    _at = -1, 0   # the workspace's device and address
 
     def allocate_workspace(self, device, stream: Optional[int] = None):
         """Allocates and clears the workspace on `stream` (default: the device's current stream)."""
@@ -49,6 +50,7 @@ class _Bound:
             if stream is None:
                 stream = torch.cuda.current_stream().cuda_stream
             L.mla_workspace_init(self.workspace.data_ptr(), self.workspace_bytes, stream)
+        self._at = self.workspace.get_device(), self.workspace.data_ptr()
         return self
 
     def read_status(self, stream: Optional[int] = None) -> int:
@@ -69,26 +71,23 @@ class _Bound:
             self.allocate_workspace(dev)
             if stream is not None:  # the allocation and its clearing are ordered on the current stream
                 torch.cuda.ExternalStream(stream, device=dev).wait_stream(torch.cuda.current_stream(dev))
-        elif self.workspace.get_device() != dev:
-            raise ValueError(f"the workspace is on {self.workspace.device}, the tensors on cuda:{dev}")
+        at, workspace = self._at
+        if at != dev:
+            raise ValueError(f"the workspace is on device {at}, the tensors on device {dev}")
         if stream is None:
             stream = torch.cuda.current_stream(dev).cuda_stream
         if dev == torch.cuda.current_device():
-            call(*args, self.workspace.data_ptr(), self.workspace_bytes, stream)
+            call(*args, workspace, self.workspace_bytes, stream)
         else:
             with torch.cuda.device(dev):
-                call(*args, self.workspace.data_ptr(), self.workspace_bytes, stream)
+                call(*args, workspace, self.workspace_bytes, stream)
 
 
 def _shapes(args) -> None:
-    """(name, tensor, dtype, shape) of every argument (an extent of -1: any). The C ABI sees bare pointers, so a
-    mismatch is caught here."""
+    """(name, tensor, dtype, shape) of every argument. The C ABI sees bare pointers, so a mismatch is caught here."""
     for name, t, dtype, shape in args:
-        got = t.shape
-        if t.dtype != dtype or (got != shape and (len(got) != len(shape) or
-                                                  any(n != e and e != -1 for n, e in zip(got, shape)))):
-            want = ", ".join("*" if e == -1 else str(e) for e in shape)
-            raise ValueError(f"{name}: {t.dtype} {tuple(got)}, needed: {dtype} ({want})")
+        if t.dtype != dtype or t.shape != shape:
+            raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, needed: {dtype} {tuple(shape)}")
 
 
 def _placed(dev: int, sources, dense) -> None:
@@ -129,7 +128,7 @@ class GqaAppend(_Bound):
         Hq, Hk, hd, D = d.num_q_heads, d.num_kv_heads, d.head_dim, d.rope_dim
         T, B, pool = k.shape[0], seq_lens.shape[0], (k_pool.shape[0], Hk, d.page_size, hd)
         sources = [("k", k, act, (T, Hk, hd)), ("v", v, act, (T, Hk, hd))]
-        dense = [("k_pool", k_pool, act, pool), ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (B, -1)),
+        dense = [("k_pool", k_pool, act, pool), ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (B, block_table.shape[-1])),
                  ("seq_lens", seq_lens, i32, (B,))]
         q_args, cu, table, positions = (None, 0, 0, None), None, None, 0
         if (q is None) != (q_out is None):
@@ -137,7 +136,7 @@ class GqaAppend(_Bound):
         if D and rope_table is None:
             raise ValueError("rope_table is needed: the dims rotate")
         if D:
-            dense.append(("rope_table", rope_table, torch.float32, (-1, D)))
+            dense.append(("rope_table", rope_table, torch.float32, (rope_table.shape[0], D)))
             table = rope_table.data_ptr()
         if cu_seqlens is not None:
             dense.append(("cu_seqlens", cu_seqlens, i32, (B + 1,)))
@@ -179,7 +178,7 @@ class LatentAppend(_Bound):
         d = self.dims
         if d.dtype == L.MLA_FP8_CACHE:
             raise ValueError("dims of the FP8 cache append with run_fp8")
-        pools = [("kv_pool", kv_pool, self._dtype, (-1, d.page_size, d.latent_rank + d.rope_dim))]
+        pools = [("kv_pool", kv_pool, self._dtype, (kv_pool.shape[0], d.page_size, d.latent_rank + d.rope_dim))]
         self._run(ckv, k_rope, pools, block_table, seq_lens, rope_table, q_rope, q_rope_out, kv_rows, cu_seqlens, stream)
 
     def run_fp8(self, ckv, k_rope, kv_codes, kv_rope, kv_scale, block_table, seq_lens, rope_table, q_rope=None,
@@ -202,14 +201,14 @@ class LatentAppend(_Bound):
         H, r, D = d.num_heads, d.latent_rank, d.rope_dim
         T, B = ckv.shape[0], seq_lens.shape[0]
         sources = [("ckv", ckv, act, (T, r))]
-        dense = [*pools, ("block_table", block_table, i32, (B, -1)), ("seq_lens", seq_lens, i32, (B,))]
+        dense = [*pools, ("block_table", block_table, i32, (B, block_table.shape[-1])), ("seq_lens", seq_lens, i32, (B,))]
         if (q_rope is None) != (q_rope_out is None):
             raise ValueError("q_rope and q_rope_out come together")
         if D and (k_rope is None or rope_table is None):
             raise ValueError("k_rope and rope_table are needed: the dims rotate")
         if D:
             sources.append(("k_rope", k_rope, act, (T, D)))
-            dense.append(("rope_table", rope_table, torch.float32, (-1, D)))
+            dense.append(("rope_table", rope_table, torch.float32, (rope_table.shape[0], D)))
         if q_rope is not None:
             sources.append(("q_rope", q_rope, act, (T, H, D)))
             dense.append(("q_rope_out", q_rope_out, act, (T, H, D)))
@@ -246,7 +245,7 @@ class _GqaPlan(_Bound):
         d, act, i32 = self.dims, self._dtype, torch.int32
         pool = (k_pool.shape[0], d.num_kv_heads, d.page_size, d.head_dim)
         args = [("q", q, act, shape), ("out", out, act, shape), ("k_pool", k_pool, act, pool),
-                ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (self.batch, -1)),
+                ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (self.batch, block_table.shape[-1])),
                 *[(name, t, i32, (n,)) for name, t, n in lengths]]
         _shapes(args)
         dev = q.get_device()
