@@ -109,9 +109,9 @@ mla_status_t mla_gqa_append(const mla_gqa_dims_t* dims, const mla_gqa_append_arg
   const dim3 grid((unsigned)gx, (unsigned)((H + p.heads_per_cta - 1) / p.heads_per_cta));
   const int half = d.rope_style == MLA_ROPE_HALF;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  if (d.dtype == MLA_BF16) pg::gqa_append_kernel<__nv_bfloat16><<<grid, pg::kAppendThreads, 0, stream>>>(p, half);
-  else pg::gqa_append_kernel<__half><<<grid, pg::kAppendThreads, 0, stream>>>(p, half);
-  return launched();
+  const dim3 block(pg::kAppendThreads);
+  return launched(d.dtype == MLA_BF16 ? launch_dependent(pg::gqa_append_kernel<__nv_bfloat16>, grid, block, 0, stream, p, half)
+                                      : launch_dependent(pg::gqa_append_kernel<__half>, grid, block, 0, stream, p, half));
 }
 
 mla_status_t mla_latent_append(const mla_dims_t* dims, int32_t rope_style, const mla_latent_append_args_t* args,
@@ -179,16 +179,14 @@ mla_status_t mla_latent_append(const mla_dims_t* dims, int32_t rope_style, const
       blocks += gx * ((p.Hq + p.heads_per_cta - 1) / p.heads_per_cta);
     }
     if (!fits32(blocks)) return MLA_ERR_UNSUPPORTED;
-    const unsigned n = (unsigned)blocks;
-    if (fp8) pg::latent_append_kernel<__nv_bfloat16, true><<<n, pg::kAppendThreads, 0, stream>>>(p, half);
-    else if (V == 8) pg::latent_append_kernel<__nv_bfloat16, false><<<n, pg::kAppendThreads, 0, stream>>>(p, half);
-    else pg::latent_append_kernel<float, false><<<n, pg::kAppendThreads, 0, stream>>>(p, half);
-  } else if (V == 8) {
-    pg::latent_append_narrow_kernel<__nv_bfloat16><<<(unsigned)p.T, pg::kNarrowThreads, 0, stream>>>(p, half);
-  } else {
-    pg::latent_append_narrow_kernel<float><<<(unsigned)p.T, pg::kNarrowThreads, 0, stream>>>(p, half);
+    const dim3 grid((unsigned)blocks), block(pg::kAppendThreads);
+    return launched(fp8      ? launch_dependent(pg::latent_append_kernel<__nv_bfloat16, true>, grid, block, 0, stream, p, half)
+                    : V == 8 ? launch_dependent(pg::latent_append_kernel<__nv_bfloat16, false>, grid, block, 0, stream, p, half)
+                             : launch_dependent(pg::latent_append_kernel<float, false>, grid, block, 0, stream, p, half));
   }
-  return launched();
+  const dim3 grid((unsigned)p.T), block(pg::kNarrowThreads);
+  return launched(V == 8 ? launch_dependent(pg::latent_append_narrow_kernel<__nv_bfloat16>, grid, block, 0, stream, p, half)
+                         : launch_dependent(pg::latent_append_narrow_kernel<float>, grid, block, 0, stream, p, half));
 }
 
 mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, const int32_t* seq_lens_host,

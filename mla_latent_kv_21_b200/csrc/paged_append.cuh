@@ -207,6 +207,10 @@ constexpr int kAppendThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) gqa_append_kernel(AppendParams p, int half_style) {
   __shared__ int32_t cu_shared[kCuShared + 1];
+  // the next grid's blocks may be placed once all of this one's are; each waits
+  // for the grid before it ahead of its first access
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
   CuSearch cs{};
   if (p.cu) {
     cs = stage_cu(p.cu, p.B, cu_shared);
@@ -257,6 +261,10 @@ __device__ __forceinline__ void turn_pair(const T* src, int i, int D, bool half,
 template <typename T>
 __global__ void __launch_bounds__(kNarrowThreads) latent_append_narrow_kernel(AppendParams p, int half_style) {
   __shared__ int32_t cu_shared[kCuShared + 1];
+  // the next grid's blocks may be placed once all of this one's are; each waits
+  // for the grid before it ahead of its first access
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
   CuSearch cs{};
   if (p.cu) {
     cs = stage_cu(p.cu, p.B, cu_shared);
@@ -304,6 +312,10 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendPar
   using VT = Vec<T>;
   constexpr int V = VT::n;
   __shared__ int32_t cu_shared[kCuShared + 1];
+  // the next grid's blocks may be placed once all of this one's are; each waits
+  // for the grid before it ahead of its first access
+  ptx::grid_launch_dependents();
+  ptx::grid_dependency_wait();
   CuSearch cs{};
   if (p.cu) {
     cs = stage_cu(p.cu, p.B, cu_shared);

@@ -111,6 +111,10 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const int bh = blockIdx.x % (p.B * p.Hk), b = bh / p.Hk, hk = bh % p.Hk;
   const int32_t pair = steps - 1 - (int32_t)(blockIdx.x / (p.B * p.Hk));
   const int tokens = kTile / p.G;                                   // of one tile
+  // the next grid's blocks may be placed once all of this one's are; each waits
+  // for the grid before it ahead of its first access
+  grid_launch_dependents();
+  grid_dependency_wait();
   const int64_t c0 = p.cu[b], c1 = p.cu[b + 1], n = c1 - c0;
   const int64_t t0 = (int64_t)pair * 2 * tokens;                    // first token of the block, in its sequence
   if (c0 < 0 || n < 0 || c1 > p.T || n > p.max_new) {
@@ -479,9 +483,8 @@ cudaError_t launch_prefill(const GqaParams& p, cudaStream_t stream) {
   const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(gqa_prefill_kernel<T, kD>), (int)S::alloc);
   if (e != cudaSuccess) return e;
   const int64_t steps = prefill_steps(p.max_new, p.G);
-  gqa_prefill_kernel<T, kD><<<(unsigned)(steps * p.B * p.Hk), kPrefillThreads, S::alloc, stream>>>(tm_q, tm_k, tm_v, p,
-                                                                                                   (int32_t)steps);
-  return cudaGetLastError();
+  return launch_dependent(gqa_prefill_kernel<T, kD>, dim3((unsigned)(steps * p.B * p.Hk)), dim3(kPrefillThreads), S::alloc,
+                          stream, tm_q, tm_k, tm_v, p, (int32_t)steps);
 }
 
 }  // namespace pg
