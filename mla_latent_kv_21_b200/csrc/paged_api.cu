@@ -19,8 +19,9 @@ struct mla_gqa_decode_plan {
 
 struct mla_gqa_prefill_plan {
   mla_gqa_dims_t dims;
-  int32_t B, max_new;
+  int32_t B, max_new, order_room;
   int64_t T;
+  size_t total;
 };
 
 namespace {
@@ -42,6 +43,15 @@ mla_status_t check_dims(const mla_gqa_dims_t& d) {
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 bool multiple(int64_t a, int64_t b, int64_t n) { return a % n == 0 && b % n == 0; }
+
+bool sm_count(int32_t* out) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess &&
+      cudaDeviceGetAttribute(out, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess)
+    return true;
+  (void)cudaGetLastError();
+  return false;
+}
 
 // A failed launch leaves no error behind for a later call to find.
 mla_status_t launched(cudaError_t e = cudaSuccess) {
@@ -203,14 +213,7 @@ mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, cons
   if (opts) o = *opts;
   int32_t sms = o.num_sms;
   if (sms < 0 || o.num_workers < 0 || o.kernel != MLA_KERNEL_AUTO) return MLA_ERR_INVALID_ARG;
-  if (sms == 0) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-      (void)cudaGetLastError();
-      return MLA_ERR_NO_DEVICE;
-    }
-  }
+  if (sms == 0 && !sm_count(&sms)) return MLA_ERR_NO_DEVICE;
   int64_t pages = 0;
   for (int b = 0; b < batch; ++b) {
     if (seq_lens_host[b] < 0) return MLA_ERR_INVALID_ARG;
@@ -292,8 +295,7 @@ mla_status_t mla_gqa_prefill_plan(const mla_gqa_dims_t* dims, int32_t batch, con
     most = std::max(most, new_tokens_host[b]);
   }
   const int G = d.num_q_heads / d.num_kv_heads;
-  if (G > 128 || !fits32(T + 2 * pg::kTile) ||
-      !fits32(pg::prefill_steps(most, G) * batch * d.num_kv_heads))
+  if (G > 128 || !fits32(T + 2 * pg::kTile) || !fits32(pg::prefill_order_room(T, batch, G) * d.num_kv_heads))
     return MLA_ERR_UNSUPPORTED;
   struct mla_gqa_prefill_plan* p = new (std::nothrow) struct mla_gqa_prefill_plan();
   if (!p) return MLA_ERR_INVALID_ARG;
@@ -301,8 +303,10 @@ mla_status_t mla_gqa_prefill_plan(const mla_gqa_dims_t* dims, int32_t batch, con
   p->B = batch;
   p->T = T;
   p->max_new = most;
+  p->order_room = (int32_t)pg::prefill_order_room(T, batch, G);
+  p->total = align_up(kHeaderBytes + p->order_room * sizeof(int2), 1024);
   *plan_out = p;
-  if (workspace_bytes) *workspace_bytes = kHeaderBytes;
+  if (workspace_bytes) *workspace_bytes = p->total;
   return MLA_OK;
 }
 
@@ -311,7 +315,7 @@ mla_status_t mla_gqa_prefill_run(mla_gqa_prefill_plan_t plan, const void* q, con
                                  const int32_t* cu_seqlens_dev, const int32_t* seq_lens_dev, void* out,
                                  void* workspace, size_t workspace_bytes, void* stream_) {
   if (!plan || !workspace || num_blocks < 1 || block_table_stride < 1) return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes < kHeaderBytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < plan->total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (plan->T == 0) return MLA_OK;
   if (!q || !k_pool || !v_pool || !block_table || !cu_seqlens_dev || !seq_lens_dev || !out || !aligned16(q) ||
       !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
@@ -335,14 +339,19 @@ mla_status_t mla_gqa_prefill_run(mla_gqa_prefill_plan_t plan, const void* q, con
   p.Hk = d.num_kv_heads;
   p.G = p.Hq / p.Hk;
   p.max_new = plan->max_new;
+  p.order_state = static_cast<int32_t*>(workspace) + 4;
+  p.order = reinterpret_cast<int2*>(static_cast<char*>(workspace) + kHeaderBytes);
+  p.order_room = plan->order_room;
+  int32_t sms = 0;
+  if (!sm_count(&sms)) return MLA_ERR_NO_DEVICE;
   p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
   p.wait_limit_ns = ptx::kWaitLimitNs;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const bool bf = d.dtype == MLA_BF16;
-  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_prefill<__nv_bfloat16, 128>(p, stream)
-                      : bf                      ? pg::launch_prefill<__nv_bfloat16, 64>(p, stream)
-                      : d.head_dim == 128       ? pg::launch_prefill<__half, 128>(p, stream)
-                                                : pg::launch_prefill<__half, 64>(p, stream);
+  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_prefill<__nv_bfloat16, 128>(p, sms, stream)
+                      : bf                      ? pg::launch_prefill<__nv_bfloat16, 64>(p, sms, stream)
+                      : d.head_dim == 128       ? pg::launch_prefill<__half, 128>(p, sms, stream)
+                                                : pg::launch_prefill<__half, 64>(p, sms, stream);
   return launched(e);
 }
 

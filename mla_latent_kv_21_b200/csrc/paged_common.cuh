@@ -44,6 +44,9 @@ struct GqaParams {
   int64_t num_blocks, T;
   int32_t bt_stride, B, Lq, Hq, Hk, G, W;
   int32_t max_new;         // prefill: largest count of the plan
+  int2* order;             // prefill workspace: (sequence, pair of tiles), longest first; NULL: one item per block
+  int32_t* order_state;    // workspace header: {items drawn, items}
+  int32_t order_room;
   float scale_log2;
   uint64_t wait_limit_ns;
 };

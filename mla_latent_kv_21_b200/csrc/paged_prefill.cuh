@@ -12,12 +12,19 @@
 //   S = Q K^T   (M 128, N 128, K d)   into the tile's 128 columns of tensor memory,
 //   P           (16-bit pairs)        over the first half of those columns,
 //   O += P V    (M 128, N d, K 128, A from tensor memory).
-// Warps: 0 producer, 1 MMA issuer, 4-7 and 8-11 the softmax of tile 0 and 1 (a
-// row per thread, running maximum and sum in fp32). The two tiles alternate:
-// while one tile's weights are computed, the tensor core works for the other.
-// The MMAs of a tile run in the order S(0), O(0), S(1), O(1), ..; one thread
-// issues them, so S(j + 1) may overwrite the P(j) that O(j) has read, and a
-// full S(j + 1) means that O(j) is complete.
+// Warps: 0 producer, 1 MMA issuer, 2 scheduler, 4-7 and 8-11 the softmax of tile
+// 0 and 1 (a row per thread, running maximum and sum in fp32). The two tiles
+// alternate: while one tile's weights are computed, the tensor core works for
+// the other. The MMAs of a tile run in the order S(0), O(0), S(1), O(1), ..; one
+// thread issues them, so S(j + 1) may overwrite the P(j) that O(j) has read, and
+// a full S(j + 1) means that O(j) is complete.
+//
+// Blocks stay: one per SM works through items (a pair of tiles), each drawn from
+// a list that a first small kernel sorts by the number of steps, longest first.
+// The next item's queries, keys and first scores come while the last one is
+// divided and stored. (A block per item took 507 us instead of PF_AFTER_8K at 8K
+// tokens and 32 heads, 65 instead of PF_AFTER_RAGGED at eight prompts of 63 to
+// 1331 tokens: about 10 us of set-up and drain per item.)
 #pragma once
 
 #include "paged_common.cuh"
@@ -35,7 +42,8 @@ template <int kD> struct PrefillSmem {
   static constexpr uint32_t q = 0;
   static constexpr uint32_t ring = 2 * tile_bytes;
   static constexpr uint32_t bars = ring + slots * tile_bytes;
-  static constexpr uint32_t misc = bars + 256;
+  static constexpr uint32_t work = bars + 320;
+  static constexpr uint32_t misc = work + 128;
   static constexpr uint32_t alloc = misc + 64 + 1024;            // the tiles start on 1 KB
   static_assert(alloc <= 227 * 1024, "shared memory of one block");
 };
@@ -98,64 +106,130 @@ __device__ __forceinline__ float max_three(float a, float b, float c) {
   return d;
 }
 
+// An item: 2 (128 / G) tokens of one sequence and one key head.
+struct Item {
+  int64_t c0;              // the sequence's first packed row
+  int64_t n, t0, ahead;    // its new tokens; the item's first; position of token t: ahead + t
+  int32_t L, b, hk;        // b < 0: no more items
+  int32_t nk0, nk1;        // steps of the two tiles (0: none, or no key is seen)
+  int32_t two_tiles, pages, any_bad;
+
+  __device__ __forceinline__ int nk() const { return max(nk0, nk1); }
+};
+
+// The new tokens of sequence b as they are, or -1 where the prefix sums are not
+// those of the packed rows or exceed the plan (told by `tell`).
+__device__ __forceinline__ int64_t new_tokens(const GqaParams& p, int32_t b, bool tell) {
+  const int64_t c0 = p.cu[b], c1 = p.cu[b + 1];
+  if (c0 >= 0 && c0 <= c1 && c1 <= p.T && c1 - c0 <= p.max_new) return c1 - c0;
+  if (tell) record_error(p.status, MLA_ERR_BOUNDS);
+  return -1;
+}
+
+// Steps of 128 keys that the tokens up to t (not included) of a sequence see.
+__device__ __forceinline__ int32_t steps_to(int64_t ahead, int64_t t) {
+  const int64_t last = ahead + t - 1;
+  return last < 0 ? 0 : (int32_t)(last / kTile) + 1;
+}
+
+// Sorts the items of a call by their steps, longest first (a counting sort; the
+// order among equals is not fixed and moves no result): p.order[i] = (sequence,
+// pair of tiles), p.order_state = {items drawn, items}.
+constexpr int kOrderThreads = 1024;
+constexpr int kOrderBuckets = 8192;
+__global__ void __launch_bounds__(kOrderThreads) gqa_prefill_order_kernel(GqaParams p) {
+  __shared__ int32_t bucket[kOrderBuckets];
+  __shared__ int32_t warp_sum[32];
+  ptx::grid_launch_dependents();
+  for (int i = threadIdx.x; i < kOrderBuckets; i += kOrderThreads) bucket[i] = 0;
+  ptx::grid_dependency_wait();
+  __syncthreads();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tokens = 2 * (kTile / p.G);
+  auto walk = [&](bool tell, auto put) {
+    for (int b = warp; b < p.B; b += 32) {
+      const int64_t n = new_tokens(p, b, tell && lane == 0);
+      const int64_t ahead = checked_len(p, b, false) - n;
+      for (int64_t i = lane; i * tokens < n; i += 32) {
+        const int32_t nk = steps_to(ahead, min(n, (i + 1) * tokens));
+        put(kOrderBuckets - 1 - min(nk, kOrderBuckets - 1), b, (int32_t)i);   // long ones first
+      }
+    }
+  };
+  walk(true, [&](int k, int, int) { atomicAdd(bucket + k, 1); });
+  __syncthreads();
+  // exclusive prefix sums over the buckets, 8 to a thread
+  constexpr int kPer = kOrderBuckets / kOrderThreads;
+  int32_t mine[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    mine[i] = sum;
+    sum += bucket[kPer * threadIdx.x + i];
+  }
+  int32_t upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  int32_t before = upto - sum, total = 0;
+  for (int i = 0; i < 32; ++i) {
+    if (i < warp) before += warp_sum[i];
+    total += warp_sum[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) bucket[kPer * threadIdx.x + i] = before + mine[i];
+  __syncthreads();
+  walk(false, [&](int k, int b, int i) {
+    const int32_t at = atomicAdd(bucket + k, 1);
+    if (at < p.order_room) p.order[at] = make_int2(b, i);
+    else record_error(p.status, MLA_ERR_BOUNDS);   // prefix sums that overlap
+  });
+  if (threadIdx.x == 0) {
+    p.order_state[0] = 0;
+    p.order_state[1] = min(total, p.order_room);
+  }
+}
+
 template <typename T, int kD>
 __global__ void __launch_bounds__(kPrefillThreads, 1)
     gqa_prefill_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-                       const __grid_constant__ CUtensorMap tm_v, GqaParams p, int32_t steps) {
+                       const __grid_constant__ CUtensorMap tm_v, GqaParams p) {
   using namespace ptx;
   using S = PrefillSmem<kD>;
   using WS = WeightScale<T>;
   constexpr int kSlots = S::slots;
   extern __shared__ uint8_t smem_raw[];
-  // ---- this block's tokens: the last ones of every sequence first (they see most keys)
-  const int bh = blockIdx.x % (p.B * p.Hk), b = bh / p.Hk, hk = bh % p.Hk;
-  const int32_t pair = steps - 1 - (int32_t)(blockIdx.x / (p.B * p.Hk));
-  const int tokens = kTile / p.G;                                   // of one tile
-  // the next grid's blocks may be placed once all of this one's are; each waits
-  // for the grid before it ahead of its first access
-  grid_launch_dependents();
-  grid_dependency_wait();
-  const int64_t c0 = p.cu[b], c1 = p.cu[b + 1], n = c1 - c0;
-  const int64_t t0 = (int64_t)pair * 2 * tokens;                    // first token of the block, in its sequence
-  if (c0 < 0 || n < 0 || c1 > p.T || n > p.max_new) {
-    if (threadIdx.x == 0 && pair == 0) record_error(p.status, MLA_ERR_BOUNDS);
-    return;
-  }
-  if (t0 >= n) return;
-  const int32_t L = checked_len(p, b, threadIdx.x == 0);
-  // tile i sees the keys up to its last token's position: nk[i] steps
-  const int64_t ahead = (int64_t)L - n;                             // position of token t: ahead + t
-  const bool two_tiles = t0 + tokens < n;
-  auto steps_of = [&](int i) {
-    const int64_t last = ahead + min(t0 + (int64_t)(i + 1) * tokens, n) - 1;
-    return last < 0 ? 0 : (int)(last / kTile) + 1;
-  };
-  const int nk0 = steps_of(0), nk1 = two_tiles ? steps_of(1) : 0, nk = max(nk0, nk1);
-  const int pages = min(pages_of(L), 2 * nk);
-  const int32_t* table = p.block_table + (int64_t)b * p.bt_stride;
-
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = smem_raw + (base - raw);
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  auto full = [&](int s) -> uint32_t { return base + S::bars + 8u * s; };
-  auto empty = [&](int s) -> uint32_t { return base + S::bars + 8u * (kSlots + s); };
-  auto q_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + i); };
-  auto s_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 2 + i); };
-  auto p_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 4 + i); };
-  auto o_full = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 6 + i); };
-  auto p_part = [&](int i) -> uint32_t { return base + S::bars + 8u * (2 * kSlots + 8 + i); };
+  auto bar = [&](int i) -> uint32_t { return base + S::bars + 8u * i; };
+  auto full = [&](int s) -> uint32_t { return bar(s); };                     // ring items
+  auto empty = [&](int s) -> uint32_t { return bar(kSlots + s); };
+  auto q_full = [&](int i) -> uint32_t { return bar(2 * kSlots + i); };      // per tile
+  auto q_empty = [&](int i) -> uint32_t { return bar(2 * kSlots + 2 + i); };
+  auto s_full = [&](int i) -> uint32_t { return bar(2 * kSlots + 4 + i); };
+  auto p_part = [&](int i) -> uint32_t { return bar(2 * kSlots + 6 + i); };
+  auto p_full = [&](int i) -> uint32_t { return bar(2 * kSlots + 8 + i); };
+  auto o_full = [&](int i) -> uint32_t { return bar(2 * kSlots + 10 + i); };
+  auto o_empty = [&](int i) -> uint32_t { return bar(2 * kSlots + 12 + i); };
+  const uint32_t w_full = bar(2 * kSlots + 14), w_empty = bar(2 * kSlots + 15);   // the work item
+  Item* work = reinterpret_cast<Item*>(gbase + S::work);
+  static_assert(sizeof(Item) <= 128 && 8 * (2 * kSlots + 16) <= 320, "shared memory layout");
   uint32_t* tslot = reinterpret_cast<uint32_t*>(gbase + S::misc);
+  const int tokens = kTile / p.G, used = tokens * p.G;              // of one tile
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 2 * kSlots; ++s) mbar_init(full(s), 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(q_full(i), 1);
-      mbar_init(s_full(i), 1);
-      mbar_init(p_part(i), 4);    // the four softmax warps of the tile
+    for (int i = 0; i < 2 * kSlots + 16; ++i) mbar_init(bar(i), 1);
+    for (int i = 0; i < 2; ++i) {        // the four softmax warps of the tile
+      mbar_init(p_part(i), 4);
       mbar_init(p_full(i), 4);
-      mbar_init(o_full(i), 1);
+      mbar_init(o_empty(i), 4);
     }
+    mbar_init(w_empty, 10);              // producer, MMA issuer, softmax warps
     fence_mbarrier_init_cluster();
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
@@ -165,287 +239,404 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     tmem_alloc<1>(base + S::misc, 512);
     tmem_relinquish<1>();
   }
-  // rows of the query tiles that no token fills
-  const int used = tokens * p.G;
+  // rows of the query tiles that no token fills; no copy writes them
   for (int i = threadIdx.x; i < 2 * (kTile - used) * (kD / 8); i += kPrefillThreads) {
     const int r = i / (kD / 8), c = i % (kD / 8), tile = r / (kTile - used), row = used + r % (kTile - used);
     *reinterpret_cast<uint4*>(gbase + S::q + tile * S::tile_bytes + (c >> 3) * (kTile * 128) + row * 128 + (c & 7) * 16) =
         make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
-  // pages whose block is out of range: their keys are not seen
-  bool bad = false;
-  for (int i = threadIdx.x; i < pages; i += kPrefillThreads) {
-    const int32_t id = table[i];
-    bad |= id < 0 || (int64_t)id >= p.num_blocks;
-  }
   tc_fence_before();
-  const bool any_bad = __syncthreads_or(bad);
+  __syncthreads();
   tc_fence_after();
   const uint32_t tbase = *tslot;
   constexpr uint32_t kTmemO = 256;       // S (and P) of tile i: columns [128 i, +128); O: [256 + d i, +d)
   bool ok = true;
-  // 384 x 168 registers at launch: 128 x 72 + 256 x 216
+  grid_launch_dependents();   // the next grid's blocks may be placed; each waits for this grid
+  grid_dependency_wait();
+
+  // Every role walks the same items in the same order. Barriers are used in
+  // phases that each role counts for itself: `items` so far, ring copies, and per
+  // tile the items and steps in which it took part.
+  uint32_t items = 0;
+  // the next item, by converged warps; the place for the one after it is free
+  // when every role has copied this one (the producer says so later, once its
+  // copies are issued, so that a block does not draw far ahead)
+  auto draw = [&](Item& x, bool free_now) {
+    if (ok) ok = mbar_wait(w_full, items & 1, p.wait_limit_ns);
+    ok = __all_sync(0xffffffffu, ok);
+    if (!ok) return false;
+    x = *work;
+    ++items;
+    __syncwarp();
+    if (free_now && lane == 0) mbar_arrive_local(w_empty);
+    return x.b >= 0;
+  };
 
   if (warp < 4) {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-  if (warp == 0) {
-    // ------------------------------------------------------------ producer --
-    const int32_t q0 = (int32_t)(c0 + t0);
-    if (lane == 0 && nk > 0) {
-      for (int i = 0; i < (two_tiles ? 2 : 1); ++i) {
-        mbar_arrive_expect_tx_local(q_full(i), (uint32_t)used * kD * 2);
-        for (int c = 0; c < kD / 64; ++c)
-          tma_load_3d(base + S::q + i * S::tile_bytes + c * (kTile * 128), &tm_q, 64 * c, hk * p.G, q0 + i * tokens, q_full(i));
+    // 384 x 168 registers at launch: 128 x 72 + 256 x 216
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 2) {
+      // ---------------------------------------------------------- scheduler --
+      Item x{};
+      int64_t ticket = blockIdx.x;
+      for (bool more = true; more && ok; ++items) {
+        x.b = -1;
+        if (p.order) {
+          if (ticket < (int64_t)p.order_state[1] * p.Hk) {
+            const int2 at = p.order[ticket / p.Hk];
+            x.b = at.x;
+            x.hk = (int32_t)(ticket % p.Hk);
+            x.t0 = (int64_t)at.y * 2 * tokens;
+          }
+        } else if (items == 0) {         // one item per block
+          const int32_t bh = blockIdx.x % (p.B * p.Hk);
+          x.b = bh / p.Hk;
+          x.hk = bh % p.Hk;
+          x.t0 = (int64_t)(blockIdx.x / (p.B * p.Hk)) * 2 * tokens;
+        }
+        if (x.b >= 0) {
+          x.n = new_tokens(p, x.b, lane == 0 && x.t0 == 0);
+          if (x.t0 >= x.n) x.b = -1;
+        }
+        more = x.b >= 0;
+        if (more) {
+          x.c0 = p.cu[x.b];
+          x.L = checked_len(p, x.b, lane == 0);
+          x.ahead = x.L - x.n;
+          x.two_tiles = x.t0 + tokens < x.n;
+          x.nk0 = steps_to(x.ahead, min(x.t0 + tokens, x.n));
+          x.nk1 = x.two_tiles ? steps_to(x.ahead, min(x.t0 + 2 * tokens, x.n)) : 0;
+          x.pages = min(pages_of(x.L), 2 * x.nk());
+          // pages whose block is out of range: their keys are not seen
+          bool bad = false;
+          for (int i = lane; i < x.pages; i += 32) {
+            const int32_t id = p.block_table[(int64_t)x.b * p.bt_stride + i];
+            bad |= id < 0 || (int64_t)id >= p.num_blocks;
+          }
+          x.any_bad = __any_sync(0xffffffffu, bad);
+          if (x.any_bad && lane == 0) record_error(p.status, MLA_ERR_BOUNDS);
+        }
+        // the last item has been read by every role, and its copies are issued
+        if (items > 0) ok = mbar_wait(w_empty, (items - 1) & 1, p.wait_limit_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          *work = x;
+          mbar_arrive_local(w_full);
+          if (more && p.order) ticket = (int64_t)gridDim.x + atomicAdd(p.order_state, 1);
+        }
+        ticket = __shfl_sync(0xffffffffu, ticket, 0);
       }
-    }
-    const int32_t nowhere = (int32_t)(p.num_blocks * p.Hk);   // past the pool: the copy fills zeros
-    int32_t ids = 0;
-    uint32_t it = 0;
-    for (int j = 0; j < nk && ok; ++j) {
-      if ((j & 15) == 0) {
-        const int x = 2 * j + lane;
-        const int32_t id = x < pages ? table[x] : -1;
-        ids = id >= 0 && (int64_t)id < p.num_blocks ? id * p.Hk + hk : nowhere;
-        if (any_bad && x < pages && ids == nowhere) record_error(p.status, MLA_ERR_BOUNDS);
-      }
-      const int32_t z0 = __shfl_sync(0xffffffffu, ids, (2 * j) & 31), z1 = __shfl_sync(0xffffffffu, ids, (2 * j + 1) & 31);
-      if (lane == 0) {
-        for (int kv = 0; kv < 2; ++kv, ++it) {
-          const int s = it % kSlots;
-          if (it >= (uint32_t)kSlots) ok = mbar_wait(empty(s), ((it / kSlots) - 1) & 1, p.wait_limit_ns);
-          if (!ok) break;
-          const uint32_t dst = base + S::ring + s * S::tile_bytes;
-          const CUtensorMap* m = kv ? &tm_v : &tm_k;
-          mbar_arrive_expect_tx_local(full(s), S::tile_bytes);
-          for (int c = 0; c < kD / 64; ++c) {
-            tma_load_3d(dst + c * (kTile * 128), m, 64 * c, 0, z0, full(s));
-            tma_load_3d(dst + c * (kTile * 128) + 8192, m, 64 * c, 0, z1, full(s));
+      if (!ok && lane == 0) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
+    } else if (warp == 0) {
+      // ----------------------------------------------------------- producer --
+      const int32_t nowhere = (int32_t)(p.num_blocks * p.Hk);   // past the pool: the copy fills zeros
+      uint32_t it = 0, q_uses[2] = {0, 0};
+      Item x;
+      while (draw(x, false)) {
+        const int32_t* table = p.block_table + (int64_t)x.b * p.bt_stride;
+        const int nk = x.nk();
+        if (lane == 0) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            if ((i ? x.nk1 : x.nk0) == 0 || !ok) continue;
+            if (q_uses[i] > 0) ok = mbar_wait(q_empty(i), (q_uses[i] - 1) & 1, p.wait_limit_ns);
+            if (!ok) continue;
+            ++q_uses[i];
+            mbar_arrive_expect_tx_local(q_full(i), (uint32_t)used * kD * 2);
+            for (int c = 0; c < kD / 64; ++c)
+              tma_load_3d(base + S::q + i * S::tile_bytes + c * (kTile * 128), &tm_q, 64 * c, x.hk * p.G,
+                          (int32_t)(x.c0 + x.t0) + i * tokens, q_full(i));
           }
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        int32_t ids = 0;
+        for (int j = 0; j < nk && ok; ++j) {
+          if ((j & 15) == 0) {
+            const int pg = 2 * j + lane;
+            const int32_t id = pg < x.pages ? table[pg] : -1;
+            ids = id >= 0 && (int64_t)id < p.num_blocks ? id * p.Hk + x.hk : nowhere;
+          }
+          const int32_t z0 = __shfl_sync(0xffffffffu, ids, (2 * j) & 31), z1 = __shfl_sync(0xffffffffu, ids, (2 * j + 1) & 31);
+          if (lane == 0) {
+            for (int kv = 0; kv < 2; ++kv, ++it) {
+              const int s = it % kSlots;
+              if (it >= (uint32_t)kSlots) ok = mbar_wait(empty(s), ((it / kSlots) - 1) & 1, p.wait_limit_ns);
+              if (!ok) break;
+              const uint32_t dst = base + S::ring + s * S::tile_bytes;
+              const CUtensorMap* m = kv ? &tm_v : &tm_k;
+              mbar_arrive_expect_tx_local(full(s), S::tile_bytes);
+              for (int c = 0; c < kD / 64; ++c) {
+                tma_load_3d(dst + c * (kTile * 128), m, 64 * c, 0, z0, full(s));
+                tma_load_3d(dst + c * (kTile * 128) + 8192, m, 64 * c, 0, z1, full(s));
+              }
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_local(w_empty);
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-    }
-    if (!ok && lane == 0) {
-      record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
-      // copies still in flight land before the block ends
-      for (uint32_t i = it > (uint32_t)kSlots ? it - kSlots : 0; i < it; ++i)
-        (void)mbar_wait(full(i % kSlots), (i / kSlots) & 1, p.wait_limit_ns);
-    }
-  } else if (warp == 1) {
-    // ----------------------------------------------------------- MMA issuer --
-    // The warp stays converged and one elected lane issues: descriptors and
-    // addresses are then uniform, and an MMA costs a few issue slots. (Issued
-    // by lane 0 of a diverged warp, the 32 MMAs of a step took 4270 cycles.)
-    if (nk > 0) {
+      if (!ok && lane == 0) {
+        record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
+        // copies still in flight land before the block ends
+        for (int i = 0; i < 2; ++i)
+          if (q_uses[i] > 0) (void)mbar_wait(q_full(i), (q_uses[i] - 1) & 1, p.wait_limit_ns);
+        for (uint32_t i = it > (uint32_t)kSlots ? it - kSlots : 0; i < it; ++i)
+          (void)mbar_wait(full(i % kSlots), (i / kSlots) & 1, p.wait_limit_ns);
+      }
+    } else if (warp == 1) {
+      // --------------------------------------------------------- MMA issuer --
+      // The warp stays converged and one elected lane issues: descriptors and
+      // addresses are then uniform, and an MMA costs a few issue slots. (Issued
+      // by lane 0 of a diverged warp, the 32 MMAs of a step took 4270 cycles;
+      // a step takes 3350 now.)
       constexpr uint32_t idesc_s = idesc16<T>(128, 128, 0, 0), idesc_o = idesc16<T>(128, kD, 0, 1);
+      constexpr std::integral_constant<int, 0> k0{};
+      constexpr std::integral_constant<int, kEarlyKeys / 16> kEarly{};
+      constexpr std::integral_constant<int, kTile / 16> kAll{};
       const bool leader = elect_one();
-      auto wait = [&](uint32_t bar, uint32_t parity) {
-        ok = ok && mbar_wait(bar, parity, p.wait_limit_ns);
+      auto wait = [&](uint32_t b, uint32_t parity) {
+        ok = ok && mbar_wait(b, parity, p.wait_limit_ns);
         ok = __all_sync(0xffffffffu, ok);
         tc_fence_after();
+      };
+      auto done = [&](uint32_t b) {
+        if (ok && leader) tc_commit<1>(b);
       };
       auto scores = [&](int i, int s) {
         if (!ok || !leader) return;
         const uint64_t a = smem_desc_sw128(base + S::q + i * S::tile_bytes, 16, 1024);
         const uint64_t k = smem_desc_sw128(base + S::ring + s * S::tile_bytes, 16, 1024);
 #pragma unroll
-        for (int x = 0; x < kD / 16; ++x) {
-          const uint64_t off = (uint64_t)((x / 4) * ((kTile * 128) >> 4) + 2 * (x % 4));
-          mma_f16<1>(tbase + 128 * i, a + off, k + off, idesc_s, x ? 1u : 0u);
+        for (int y = 0; y < kD / 16; ++y) {
+          const uint64_t off = (uint64_t)((y / 4) * ((kTile * 128) >> 4) + 2 * (y % 4));
+          mma_f16<1>(tbase + 128 * i, a + off, k + off, idesc_s, y ? 1u : 0u);
         }
         tc_commit<1>(s_full(i));
       };
-      auto values = [&](int i, int s, bool more, auto x0, auto x1) {
+      auto values = [&](int i, int s, bool more, auto from, auto to) {
         if (!ok || !leader) return;
         const uint64_t v = smem_desc_sw128(base + S::ring + s * S::tile_bytes, kTile * 128, 1024);
 #pragma unroll
-        for (int x = x0; x < x1; ++x)
-          mma_ts(tbase + kTmemO + kD * i, tbase + 128 * i + 8 * x, v + (uint64_t)(128 * x), idesc_o, more || x ? 1u : 0u);
+        for (int y = from; y < to; ++y)
+          mma_ts(tbase + kTmemO + kD * i, tbase + 128 * i + 8 * y, v + (uint64_t)(128 * y), idesc_o, more || y ? 1u : 0u);
       };
-      auto done = [&](uint32_t bar) {
-        if (ok && leader) tc_commit<1>(bar);
-      };
-      constexpr std::integral_constant<int, 0> k0{};
-      constexpr std::integral_constant<int, kEarlyKeys / 16> kEarly{};
-      constexpr std::integral_constant<int, kTile / 16> kAll{};
-      uint32_t it = 0;                   // the next ring item
-      auto arrived = [&]() {
+      uint32_t it = 0, uses[2] = {0, 0}, steps[2] = {0, 0};
+      auto arrived = [&]() {             // the next ring item's slot
         wait(full(it % kSlots), (it / kSlots) & 1);
         return (int)(it++ % kSlots);
       };
-      const int s = arrived();
-      // a tile that sees no key is waited for too: its copy lands before the block ends
-      wait(q_full(0), 0);
-      if (nk0 > 0) scores(0, s);
-      if (two_tiles) wait(q_full(1), 0);
-      if (nk1 > 0) scores(1, s);
-      done(empty(s));
-      for (int j = 0; j < nk && ok; ++j) {
-        const int vs = arrived();
-        int ks = 0;
-        if (j < nk0) {
-          wait(p_part(0), j & 1);
-          values(0, vs, j > 0, k0, kEarly);
-          wait(p_full(0), j & 1);
-          values(0, vs, j > 0, kEarly, kAll);
-          if (j + 1 == nk0) done(o_full(0));
+      Item x;
+      while (draw(x, true)) {
+        const int nk = x.nk();
+        if (nk == 0) continue;
+        const int ks0 = arrived();
+        // the first scores of a tile; its query slot is free again after its last
+        auto begin = [&](int i, int n) {
+          if (n == 0) return;
+          wait(q_full(i), uses[i]++ & 1);
+          scores(i, ks0);
+          if (n == 1) done(q_empty(i));
+        };
+        begin(0, x.nk0);
+        begin(1, x.nk1);
+        done(empty(ks0));
+        // O = P V of step j; the last item's O has been read before the first
+        auto step = [&](int i, int n, int j, int vs) {
+          if (j >= n) return;
+          if (j == 0 && uses[i] > 1) wait(o_empty(i), (uses[i] - 2) & 1);
+          wait(p_part(i), steps[i] & 1);
+          values(i, vs, j > 0, k0, kEarly);
+          wait(p_full(i), steps[i]++ & 1);
+          values(i, vs, j > 0, kEarly, kAll);
+          if (j + 1 == n) done(o_full(i));
+        };
+        auto next_scores = [&](int i, int n, int j, int ks) {
+          if (j + 1 >= n) return;
+          scores(i, ks);
+          if (j + 2 == n) done(q_empty(i));
+        };
+        for (int j = 0; j < nk && ok; ++j) {
+          const int vs = arrived();
+          int ks = 0;
+          step(0, x.nk0, j, vs);
+          if (j + 1 < nk) {
+            ks = arrived();
+            next_scores(0, x.nk0, j, ks);
+          }
+          step(1, x.nk1, j, vs);
+          done(empty(vs));
+          if (j + 1 < nk) {
+            next_scores(1, x.nk1, j, ks);
+            done(empty(ks));
+          }
         }
-        if (j + 1 < nk) {
-          ks = arrived();
-          if (j + 1 < nk0) scores(0, ks);
-        }
-        if (j < nk1) {
-          wait(p_part(1), j & 1);
-          values(1, vs, j > 0, k0, kEarly);
-          wait(p_full(1), j & 1);
-          values(1, vs, j > 0, kEarly, kAll);
-          if (j + 1 == nk1) done(o_full(1));
-        }
-        done(empty(vs));
-        if (j + 1 < nk) {
-          if (j + 1 < nk1) scores(1, ks);
-          done(empty(ks));
-        }
+        if (!ok) break;
       }
+      // the last commit has arrived before the block ends
+      if (it > 0) wait(empty((it - 1) % kSlots), ((it - 1) / kSlots) & 1);
       if (!ok && lane == 0) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // -------------------------------------------------------------- softmax --
     const int tile = (warp - 4) >> 2;
     const int row = 32 * (warp & 3) + lane;
-    const int64_t t = t0 + (int64_t)tile * tokens + row / p.G;      // this row's token, in its sequence
-    const bool real = row < used && t < n;
-    // keys that the row sees; a row without a query is computed and not stored
-    const int64_t sees = real ? max((int64_t)0, ahead + t + 1) : (int64_t)1 << 40;
-    const int steps_here = tile ? nk1 : nk0;
     const uint32_t s_cols = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + 128 * tile;
     const uint32_t o_cols = tbase + ((uint32_t)(32 * (warp & 3)) << 16) + kTmemO + kD * tile;
-    float m = -INFINITY, l = 0.f;
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-      if (ok) ok = mbar_wait(bar, parity, p.wait_limit_ns);
+    uint32_t it0 = 0, uses = 0, steps = 0;
+    auto wait = [&](uint32_t b, uint32_t parity) {
+      if (ok) ok = mbar_wait(b, parity, p.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ok);
     };
-    for (int j = 0; j < steps_here; ++j) {
-      wait(s_full(tile), j & 1);
+    const int row_token = tile * tokens + row / p.G;
+    for (;;) {
+      int32_t sees, nk, L, clear_from;   // clear_from: the step from which on this tile clears the cache's last values
+      int32_t it_next;
+      const int32_t* table = nullptr;    // of a sequence with pages that are out of range
+      int32_t pages = 0;
+      T* out = nullptr;                  // this row's, if it is one of the item's
+      {
+        Item x;
+        if (!draw(x, true)) break;
+        // keys that the row sees; a row without a query is computed and not stored
+        const int64_t t = x.t0 + row_token;                           // this row's token, in its sequence
+        const bool real = row < used && t < x.n;
+        sees = real ? (int32_t)max((int64_t)0, x.ahead + t + 1) : 0x7fffffff;
+        if (real) out = static_cast<T*>(p.out) + ((x.c0 + t) * p.Hq + x.hk * p.G + row % p.G) * (int64_t)kD;
+        nk = tile ? x.nk1 : x.nk0;
+        L = x.L;
+        clear_from = tile ? x.nk0 : 0;
+        it_next = it0 + 2 * x.nk();
+        if (x.any_bad) {
+          table = p.block_table + (int64_t)x.b * p.bt_stride;
+          pages = x.pages;
+        }
+      }
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nk; ++j) {
+        wait(s_full(tile), steps++ & 1);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t r[kTile];
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) tmem_ld32(s_cols + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
+        tmem_wait_ld();
+        const int32_t left = sees - j * kTile;
+        if (left < kTile) {
+#pragma unroll
+          for (int c = 0; c < kTile; ++c)
+            if (c >= left) r[c] = 0xff800000u;
+        }
+        if (table) {
+          for (int half = 0; half < 2; ++half) {
+            const int pg = 2 * j + half;
+            const int32_t id = pg < pages ? table[pg] : 0;
+            if (id < 0 || (int64_t)id >= p.num_blocks) {
+#pragma unroll
+              for (int c = 0; c < kTile; ++c)
+                if (c / kPage == half) r[c] = 0xff800000u;
+            }
+          }
+        }
+        float y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < kTile; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            y[e] = max_three(y[e], __uint_as_float(r[c + 2 * e]), __uint_as_float(r[c + 2 * e + 1]));
+        const float top = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) * p.scale_log2;
+        const bool move = top > m + WS::lazy;      // also a row's first visible key (m = -inf)
+        const float mn = move ? top : m;
+        if (__any_sync(0xffffffffu, move && l > 0.f)) {
+          // the products up to step j - 1 are complete (S(j) is), and no other is under way
+          const float a = m == mn ? 1.f : ex2_approx(m - mn);
+          l *= a;
+#pragma unroll 1
+          for (int c = 0; c < kD; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_cols + c, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
+            tmem_st32(o_cols + c, o);
+          }
+        }
+        m = mn;
+        if (L - j * kTile < kTile && j >= clear_from) {
+          // the cache's last step: values of slots without a token may hold
+          // anything, and 0 times NaN is not 0. The first tile to use them
+          // clears them before its weights are handed over.
+          const uint32_t it = it0 + 2 * j + 1;
+          wait(full(it % kSlots), (it / kSlots) & 1);
+          if (ok)
+            for (int i = row; i < (kTile - (L - j * kTile)) * (kD / 8); i += 128) {
+              const int z = kTile - 1 - i / (kD / 8), c = i % (kD / 8);
+              *reinterpret_cast<uint4*>(gbase + S::ring + it % kSlots * S::tile_bytes + (c >> 3) * (kTile * 128) + z * 128 +
+                                        (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+          fence_proxy_async_smem();
+        }
+        const float shift = m == -INFINITY ? 0.f : WS::bias - m;
+        const uint64_t sc = two(p.scale_log2, p.scale_log2), sh = two(shift, shift);
+        uint64_t sum0 = two(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+        for (int c = 0; c < kTile; c += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float2 a = apart(fma_two(two(__uint_as_float(r[c + e]), __uint_as_float(r[c + e + 1])), sc, sh));
+            const float2 d = apart(fma_two(two(__uint_as_float(r[c + e + 2]), __uint_as_float(r[c + e + 3])), sc, sh));
+            const float y0 = ex2_approx(a.x), y1 = ex2_approx(a.y), y2 = ex2_approx(d.x), y3 = ex2_approx(d.y);
+            sum0 = add_two(sum0, two(y0, y1));
+            sum1 = add_two(sum1, two(y2, y3));
+            w[e / 2] = Pack<T>::of(y0, y1);
+            w[e / 2 + 1] = Pack<T>::of(y2, y3);
+          }
+          tmem_st16(s_cols + c / 2, w);   // over scores that are in registers
+          if (c + 32 == kEarlyKeys) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_local(p_part(tile));
+          }
+        }
+        const float2 u0 = apart(sum0), u1 = apart(sum1);
+        l += (u0.x + u0.y) + (u1.x + u1.y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_local(p_full(tile));
+      }
+      it0 = it_next;
+      // ---- O / l, read before the next item's first product may overwrite it
+      if (nk > 0) wait(o_full(tile), uses++ & 1);
       if (!ok) break;
       tc_fence_after();
-      uint32_t r[kTile];
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) tmem_ld32(s_cols + c, *reinterpret_cast<uint32_t(*)[32]>(r + c));
-      tmem_wait_ld();
-      const int64_t left = sees - (int64_t)j * kTile;
-      if (left < kTile) {
-#pragma unroll
-        for (int c = 0; c < kTile; ++c)
-          if (c >= (int)left) r[c] = 0xff800000u;
-      }
-      if (any_bad) {
-        for (int half = 0; half < 2; ++half) {
-          const int x = 2 * j + half;
-          const int32_t id = x < pages ? table[x] : 0;
-          if (id < 0 || (int64_t)id >= p.num_blocks) {
-#pragma unroll
-            for (int c = 0; c < kTile; ++c)
-              if (c / kPage == half) r[c] = 0xff800000u;
-          }
-        }
-      }
-      float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < kTile; c += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          x[e] = max_three(x[e], __uint_as_float(r[c + 2 * e]), __uint_as_float(r[c + 2 * e + 1]));
-      const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * p.scale_log2;
-      const bool move = top > m + WS::lazy;      // also a row's first visible key (m = -inf)
-      const float mn = move ? top : m;
-      if (__any_sync(0xffffffffu, move && l > 0.f)) {
-        // the products up to step j - 1 are complete (S(j) is), and no other is under way
-        const float a = m == mn ? 1.f : ex2_approx(m - mn);
-        l *= a;
-#pragma unroll 1
-        for (int c = 0; c < kD; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_cols + c, o);
-          tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * a);
-          tmem_st32(o_cols + c, o);
-        }
-      }
-      m = mn;
-      if ((j + 1) * kTile > L && (tile == 0 || j >= nk0)) {
-        // the cache's last step: values of slots without a token may hold
-        // anything, and 0 times NaN is not 0. The first tile to use them
-        // clears them before its weights are handed over.
-        const int s = (2 * j + 1) % kSlots;
-        wait(full(s), ((2 * j + 1) / kSlots) & 1);
-        if (ok)
-          for (int i = row; i < ((j + 1) * kTile - L) * (kD / 8); i += 128) {
-            const int x = kTile - 1 - i / (kD / 8), c = i % (kD / 8);
-            *reinterpret_cast<uint4*>(gbase + S::ring + s * S::tile_bytes + (c >> 3) * (kTile * 128) + x * 128 + (c & 7) * 16) =
-                make_uint4(0, 0, 0, 0);
-          }
-        fence_proxy_async_smem();
-      }
-      const float shift = m == -INFINITY ? 0.f : WS::bias - m;
-      const uint64_t sc = two(p.scale_log2, p.scale_log2), sh = two(shift, shift);
-      uint64_t sum0 = two(0.f, 0.f), sum1 = sum0;
-#pragma unroll
-      for (int c = 0; c < kTile; c += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int e = 0; e < 32; e += 4) {
-          const float2 a = apart(fma_two(two(__uint_as_float(r[c + e]), __uint_as_float(r[c + e + 1])), sc, sh));
-          const float2 d = apart(fma_two(two(__uint_as_float(r[c + e + 2]), __uint_as_float(r[c + e + 3])), sc, sh));
-          const float y0 = ex2_approx(a.x), y1 = ex2_approx(a.y), y2 = ex2_approx(d.x), y3 = ex2_approx(d.y);
-          sum0 = add_two(sum0, two(y0, y1));
-          sum1 = add_two(sum1, two(y2, y3));
-          w[e / 2] = Pack<T>::of(y0, y1);
-          w[e / 2 + 1] = Pack<T>::of(y2, y3);
-        }
-        tmem_st16(s_cols + c / 2, w);   // over scores that are in registers
-        if (c + 32 == kEarlyKeys) {
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_local(p_part(tile));
-        }
-      }
-      const float2 u0 = apart(sum0), u1 = apart(sum1);
-      l += (u0.x + u0.y) + (u1.x + u1.y);
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_local(p_full(tile));
-    }
-    // ---- O / l
-    if (steps_here > 0) wait(o_full(tile), 0);
-    if (ok) {
-      tc_fence_after();
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      T* out = static_cast<T*>(p.out) + ((c0 + t) * p.Hq + hk * p.G + row % p.G) * (int64_t)kD;
 #pragma unroll 1
       for (int c = 0; c < kD; c += 32) {
         uint32_t o[32];
-        if (steps_here > 0) {
+        if (nk > 0) {
           tmem_ld32(o_cols + c, o);
           tmem_wait_ld();
         }
-        if (!real) continue;
+        if (!out) continue;
 #pragma unroll
         for (int e = 0; e < 32; e += 8) {
           uint32_t w[4];
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
-            w[x] = l > 0.f ? Pack<T>::of(__uint_as_float(o[e + 2 * x]) * inv, __uint_as_float(o[e + 2 * x + 1]) * inv) : 0u;
+          for (int i = 0; i < 4; ++i)
+            w[i] = l > 0.f ? Pack<T>::of(__uint_as_float(o[e + 2 * i]) * inv, __uint_as_float(o[e + 2 * i + 1]) * inv) : 0u;
           *reinterpret_cast<uint4*>(out + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (nk > 0 && lane == 0) mbar_arrive_local(o_empty(tile));
     }
     if (!ok && lane == 0) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
   }
@@ -469,22 +660,33 @@ inline bool query_map(CUtensorMap* m, const void* q, int64_t T, int Hq, int G, i
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Blocks of one launch: a pair of tiles of every sequence's longest possible count, per key head.
-inline int64_t prefill_steps(int32_t max_new, int G) { return (max_new + 2 * (kTile / G) - 1) / (2 * (kTile / G)); }
+// Pairs of tiles of the longest count that a plan allows.
+inline int64_t prefill_pairs(int32_t max_new, int G) { return (max_new + 2 * (kTile / G) - 1) / (2 * (kTile / G)); }
+
+// Items whose order a workspace has room for: pairs of tiles of any prefix sums over T rows.
+inline int64_t prefill_order_room(int64_t T, int32_t B, int G) { return T / (2 * (kTile / G)) + B; }
 
 template <typename T, int kD>
-cudaError_t launch_prefill(const GqaParams& p, cudaStream_t stream) {
+cudaError_t launch_prefill(GqaParams p, int32_t sms, cudaStream_t stream) {
   using S = PrefillSmem<kD>;
   constexpr bool bf16 = std::is_same<T, __nv_bfloat16>::value;
   CUtensorMap tm_q, tm_k, tm_v;
   if (!query_map(&tm_q, p.q, p.T, p.Hq, p.G, kD, bf16) ||
       !pool_map(&tm_k, p.k_pool, p.num_blocks * p.Hk, kD, bf16) || !pool_map(&tm_v, p.v_pool, p.num_blocks * p.Hk, kD, bf16))
     return cudaErrorInvalidValue;
-  const cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(gqa_prefill_kernel<T, kD>), (int)S::alloc);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(gqa_prefill_kernel<T, kD>), (int)S::alloc);
   if (e != cudaSuccess) return e;
-  const int64_t steps = prefill_steps(p.max_new, p.G);
-  return launch_dependent(gqa_prefill_kernel<T, kD>, dim3((unsigned)(steps * p.B * p.Hk)), dim3(kPrefillThreads), S::alloc,
-                          stream, tm_q, tm_k, tm_v, p, (int32_t)steps);
+  // as many items as blocks fit at once: each takes its own, no order is needed
+  int64_t blocks = prefill_pairs(p.max_new, p.G) * p.B * p.Hk;
+  if (blocks <= sms) {
+    p.order = nullptr;
+  } else {
+    blocks = std::min<int64_t>(sms, (int64_t)p.order_room * p.Hk);
+    e = launch_dependent(gqa_prefill_order_kernel, dim3(1), dim3(kOrderThreads), 0, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dependent(gqa_prefill_kernel<T, kD>, dim3((unsigned)blocks), dim3(kPrefillThreads), S::alloc, stream, tm_q, tm_k,
+                          tm_v, p);
 }
 
 }  // namespace pg

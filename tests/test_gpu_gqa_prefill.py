@@ -146,6 +146,76 @@ def test_bad_metadata_is_recorded(cuda_device):
     check_attention(out[:100], q[:100], *seqs[0], 128 ** -0.5, torch.bfloat16, "first")
 
 
+# More items than the device has blocks: every block draws several from the sorted list.
+MANY = [(700, 900), (1, 1), (0, 30), (1300, 1300), (64, 500), (333, 333), (1, 2000), (900, 901), (0, 0), (65, 64), (1100, 1500),
+        (20, 0)]
+
+
+@pytest.mark.parametrize("dtype,Hk,G,d", [("bf16", 4, 4, 128), ("fp16", 8, 7, 64), ("bf16", 8, 1, 128), ("fp16", 2, 40, 128),
+                                          ("bf16", 1, 128, 64)])
+def test_many_items(cuda_device, dtype, Hk, G, d):
+    new, lens = [c[0] for c in MANY], [c[1] for c in MANY]
+    dev, q, cu, seqs = _inputs(new, lens, Hk, G, d, TYPES[dtype], 31, cuda_device, extra_rows=9)
+    counts = list(new)
+    counts[2] = 9    # rows that the call's prefix sums leave over
+    plan = M.GqaPrefillPlan(_dims(Hk, G, d, dtype), counts).allocate_workspace(cuda_device)
+    out, again = torch.full_like(dev["q"], 7.0), torch.full_like(dev["q"], 7.0)
+    _run(plan, dev, out)
+    _run(plan, dev, again)
+    assert plan.read_status() == 0 and torch.equal(out, again)
+    assert (out[-9:] == 7.0).all()
+    _check(out, q, cu, seqs, d, dtype, "many items")
+
+
+def test_many_items_with_bad_metadata(cuda_device):
+    new, lens = [1000, 1200, 900, 800], [1000, 1300, 900, 2000]
+    dev, q, cu, seqs = _inputs(new, lens, 4, 4, 128, torch.bfloat16, 32, cuda_device)
+    plan = M.GqaPrefillPlan(_dims(4, 4, 128, "bf16"), new).allocate_workspace(cuda_device)
+    out = torch.full_like(dev["q"], 7.0)
+
+    def check(bad):
+        assert plan.read_status() == M.MLA_ERR_BOUNDS and plan.read_status() == 0
+        for b in range(4):
+            if b not in bad:
+                rows = slice(cu[b], cu[b + 1])
+                check_attention(out[rows], q[rows], *seqs[b], 128 ** -0.5, torch.bfloat16, f"sequence {b}")
+
+    dev["sl"][1] = -1
+    _run(plan, dev, out)
+    check([1])
+    assert (out[1000:2200] == 0).all()
+    dev["sl"][1] = 1300
+    keep = dev["bt"].clone()
+    dev["bt"][3, 5], dev["bt"][3, 6] = -1, dev["kp"].shape[0]
+    _run(plan, dev, out)
+    check([3])
+    k, v = seqs[3]
+    seen = torch.tensor([j for j in range(2000) if j // 64 not in (5, 6)])
+    check_attention(out[-50:], q[-50:], k[seen], v[seen], 128 ** -0.5, torch.bfloat16, "the pages that remain")
+    dev["bt"].copy_(keep)
+    out.fill_(7.0)
+    dev["cu"][2] = 2300     # 1300 and 800 new tokens: the first is above the plan's largest count
+    _run(plan, dev, out)
+    check([1, 2])
+    assert (out[1000:2300] == 7.0).all()
+    out.fill_(7.0)
+    dev["cu"].copy_(torch.tensor([0, 1000, 0, 1000, 1800], dtype=torch.int32))   # sums that fall
+    _run(plan, dev, out)
+    assert plan.read_status() == M.MLA_ERR_BOUNDS
+
+
+def test_many_sequences(cuda_device):
+    """700 short prompts, some empty."""
+    new = [(b * 5) % 9 for b in range(700)]
+    lens = [n + (b * 3) % 70 for b, n in enumerate(new)]
+    dev, q, cu, seqs = _inputs(new, lens, 2, 4, 64, torch.float16, 33, cuda_device)
+    plan = M.GqaPrefillPlan(_dims(2, 4, 64, "fp16"), new).allocate_workspace(cuda_device)
+    out = torch.full_like(dev["q"], float("nan"))
+    _run(plan, dev, out)
+    assert plan.read_status() == 0
+    _check(out, q, cu, seqs, 64, "fp16", "many sequences")
+
+
 def test_offsets_past_32_bits(cuda_device):
     new, lens, Hk, d = [150, 64], [150, 100], 8, 128
     blocks = 2 ** 31 // (Hk * 64 * d) + 40

@@ -85,7 +85,7 @@ def test_null_and_misaligned_pointers():
     good = dict(plan=plan, q=fake, k_pool=fake, v_pool=fake, num_blocks=4, block_table=fake, block_table_stride=2,
                 cu_seqlens_dev=fake, seq_lens_dev=fake, out=fake, workspace=fake, workspace_bytes=ws)
     for name, bad, status in [("q", fake + 8, 1), ("k_pool", 0, 1), ("cu_seqlens_dev", 0, 1), ("out", 0, 1),
-                              ("workspace_bytes", 1023, 3), ("num_blocks", 2 ** 31, 2)]:
+                              ("workspace_bytes", ws - 1, 3), ("num_blocks", 2 ** 31, 2)]:
         with pytest.raises(M.MlaError) as e:
             L.mla_gqa_prefill_run(**dict(good, **{name: bad}))
         assert e.value.status == status, (name, bad)
