@@ -22,9 +22,21 @@
 // Blocks stay: one per SM works through items (a pair of tiles), each drawn from
 // a list that a first small kernel sorts by the number of steps, longest first.
 // The next item's queries, keys and first scores come while the last one is
-// divided and stored. (A block per item took 507 us instead of PF_AFTER_8K at 8K
-// tokens and 32 heads, 65 instead of PF_AFTER_RAGGED at eight prompts of 63 to
-// 1331 tokens: about 10 us of set-up and drain per item.)
+// divided and stored. (With a block per item, about 10 us of set-up and drain
+// each: 64 us instead of 51 at eight prompts of 63 to 1331 tokens, 480 instead of
+// 427 at 8K tokens and 32 heads.)
+//
+// What bounds it: a step of two tiles takes 3190 cycles (both head sizes). The
+// chain of one tile is scores in tensor memory -> registers 70, maximum 370,
+// weights 1450 (1024 of special-function unit, shared with the other tile's
+// warps), P V and Q K^T 1180; the tensor core is busy for 2048 of the cycles at
+// d = 128. At 8K tokens that is 427 us from cold (1290 TFLOP/s); in a loop the
+// power cap lowers the clock to 1.67 GHz and it takes 480 to 525 us. Tried and
+// no faster: the maximum found beside the first weights, with those made again
+// where it moves (3370 cycles); for d = 64, weights in columns of their own, so
+// that S(j + 1) is computed during the softmax of step j (3700 cycles: the two
+// tiles fall into step and share the special-function unit); a quarter or half of
+// the exponentials by a polynomial (more instructions, more power).
 #pragma once
 
 #include "paged_common.cuh"
