@@ -30,7 +30,7 @@
  * Ownership, streams, graph capture and errors are those of mla_decode.h: the
  * caller owns every device buffer, nothing allocates or synchronises, and what
  * is wrong on the device (a block id outside [0, num_blocks), a length outside
- * [0, 64 block_table_stride], rows of cu_seqlens outside the packed tensors, a
+ * [0, 64 block_table_stride] or above 2^31 - 4096, rows of cu_seqlens outside the packed tensors, a
  * position outside the rotation table) is recorded as MLA_ERR_BOUNDS in the
  * workspace's status word (mla_decode_read_status), while the work it concerns
  * is skipped. Calls run on the current device, which must be the stream's. A
@@ -129,7 +129,9 @@ typedef struct {
  * cache (r = 512, D = 64), where a token's scale is
  *   s = max(max_i |cKV_i| / 448, 2^-64),
  * its codes are e4m3(cKV / s) (round to nearest even) and its RoPE key is
- * stored as bf16(k_rope / s). d_rope must be even. Any alignment; 16-byte
+ * stored as bf16(k_rope / s). Only the tokens' own slots are written: clear a
+ * fresh pool once, since the latent decode weights unused slots of a page by 0
+ * and needs them finite. d_rope must be even. Any alignment; 16-byte
  * aligned pointers and strides (and r, D multiples of 16) take the wide path,
  * and the FP8 cache needs them. One kernel on `stream`. */
 mla_status_t mla_latent_append(const mla_dims_t* dims, int32_t rope_style,

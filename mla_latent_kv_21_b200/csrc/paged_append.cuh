@@ -67,7 +67,7 @@ __device__ __forceinline__ Place place_of(const AppendParams& p, const CuSearch&
     i = t - (int64_t)b * p.Lq;
   }
   const int64_t L = p.seq_lens[b], pos = L - n + i;
-  bool ok = L >= n && L <= (int64_t)p.bt_stride * kPage && (p.D == 0 || pos < p.table_rows);
+  bool ok = L >= n && L <= kMaxLen && L <= (int64_t)p.bt_stride * kPage && (p.D == 0 || pos < p.table_rows);
   if (ok) {
     r.block = p.block_table[(int64_t)b * p.bt_stride + pos / kPage];
     r.slot = (int32_t)(pos % kPage);
@@ -207,10 +207,11 @@ constexpr int kAppendThreads = 128;
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) gqa_append_kernel(AppendParams p, int half_style) {
   __shared__ int32_t cu_shared[kCuShared + 1];
-  // the next grid's blocks may be placed once all of this one's are; each waits
-  // for the grid before it ahead of its first access
-  ptx::grid_launch_dependents();
+  // Every access waits for the grid before this one; only then may the next
+  // grid's blocks be placed, so that what they read ahead of their own wait
+  // (weights) is past whatever wrote it.
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   CuSearch cs{};
   if (p.cu) {
     cs = stage_cu(p.cu, p.B, cu_shared);
@@ -261,10 +262,11 @@ __device__ __forceinline__ void turn_pair(const T* src, int i, int D, bool half,
 template <typename T>
 __global__ void __launch_bounds__(kNarrowThreads) latent_append_narrow_kernel(AppendParams p, int half_style) {
   __shared__ int32_t cu_shared[kCuShared + 1];
-  // the next grid's blocks may be placed once all of this one's are; each waits
-  // for the grid before it ahead of its first access
-  ptx::grid_launch_dependents();
+  // Every access waits for the grid before this one; only then may the next
+  // grid's blocks be placed, so that what they read ahead of their own wait
+  // (weights) is past whatever wrote it.
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   CuSearch cs{};
   if (p.cu) {
     cs = stage_cu(p.cu, p.B, cu_shared);
@@ -312,10 +314,11 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendPar
   using VT = Vec<T>;
   constexpr int V = VT::n;
   __shared__ int32_t cu_shared[kCuShared + 1];
-  // the next grid's blocks may be placed once all of this one's are; each waits
-  // for the grid before it ahead of its first access
-  ptx::grid_launch_dependents();
+  // Every access waits for the grid before this one; only then may the next
+  // grid's blocks be placed, so that what they read ahead of their own wait
+  // (weights) is past whatever wrote it.
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   CuSearch cs{};
   if (p.cu) {
     cs = stage_cu(p.cu, p.B, cu_shared);

@@ -91,10 +91,12 @@ __device__ __forceinline__ int32_t sequence_of(const CuSearch& s, const int32_t*
 template <typename T> struct WeightScale { static constexpr float bias = 0.f, lazy = 8.f; };
 template <> struct WeightScale<__half> { static constexpr float bias = 8.f, lazy = 6.f; };
 
-// The tokens of sequence b; a length out of range counts as 0 (`tell`: record it).
+// The tokens of sequence b; a length out of range counts as 0 (`tell`: record
+// it). Lengths stay so far below 2^31 that a step past them is still an int32.
+constexpr int32_t kMaxLen = 0x7ffff000;
 __device__ __forceinline__ int32_t checked_len(const GqaParams& p, int32_t b, bool tell) {
   const int32_t L = p.seq_lens[b];
-  if (L >= 0 && (int64_t)L <= (int64_t)p.bt_stride * kPage) return L;
+  if (L >= 0 && L <= kMaxLen && (int64_t)L <= (int64_t)p.bt_stride * kPage) return L;
   if (tell) record_error(p.status, MLA_ERR_BOUNDS);
   return 0;
 }

@@ -154,10 +154,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  // the next grid's blocks may be placed once all of this one's are; each waits
-  // for the grid before it ahead of its first access
-  grid_launch_dependents();
+  // Every access waits for the grid before this one; only then may the next
+  // grid's blocks be placed, so that what they read ahead of their own wait
+  // (weights) is past whatever wrote it.
   grid_dependency_wait();
+  grid_launch_dependents();
   // ---- the page line: every thread sums the pages of a run of sequences, a scan gives the runs' places
   const int per = (p.B + kDecodeThreads - 1) / kDecodeThreads;
   const int b_lo = min(p.B, (int)threadIdx.x * per), b_hi = min(p.B, b_lo + per);
@@ -242,6 +243,13 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     const int g = lane >> 2, t4 = lane & 3;
     const int row0 = 16 * tile + g, row1 = row0 + 8;
     const int key0 = part * kKeys;           // this warp's first key of a page
+    // per row, from an item's first query: its elements' offset, and how many keys
+    // less than the item's length its token sees (a row past `rows` stands for the
+    // last token: finite, never stored)
+    const bool real0 = row0 < rows, real1 = row1 < rows;
+    const int last0 = real0 ? row0 : rows - 1, last1 = real1 ? row1 : rows - 1;
+    const int off0 = (last0 / p.G * p.Hq + last0 % p.G) * kD + 2 * t4, off1 = (last1 / p.G * p.Hq + last1 % p.G) * kD + 2 * t4;
+    const int less0 = p.Lq - 1 - last0 / p.G, less1 = p.Lq - 1 - last1 / p.G;
     float* sm = reinterpret_cast<float*>(gbase + S::ml);
     float* sl = sm + 64;
     float* join = reinterpret_cast<float*>(gbase + S::join);
@@ -252,24 +260,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     int2 tail = make_int2(-1, 0);
     for (; have; have = seg.next(p)) {
       uint32_t q[kD / 16][4];
+      const int64_t item = ((int64_t)seg.b * p.Lq * p.Hq + seg.h * p.G) * kD;   // its first query's elements
       {
-        auto src = [&](int r) {
-          return static_cast<const T*>(p.q) +
-                 (((int64_t)seg.b * p.Lq + r / p.G) * p.Hq + seg.h * p.G + r % p.G) * kD + 2 * t4;
-        };
-        const T* a = src(row0 < rows ? row0 : 0);
-        const T* c = src(row1 < rows ? row1 : 0);
+        const T* a = static_cast<const T*>(p.q) + item + off0;
+        const T* c = static_cast<const T*>(p.q) + item + off1;
 #pragma unroll
         for (int k = 0; k < kD / 16; ++k) {
-          q[k][0] = row0 < rows ? *reinterpret_cast<const uint32_t*>(a + 16 * k) : 0u;
-          q[k][1] = row1 < rows ? *reinterpret_cast<const uint32_t*>(c + 16 * k) : 0u;
-          q[k][2] = row0 < rows ? *reinterpret_cast<const uint32_t*>(a + 16 * k + 8) : 0u;
-          q[k][3] = row1 < rows ? *reinterpret_cast<const uint32_t*>(c + 16 * k + 8) : 0u;
+          q[k][0] = *reinterpret_cast<const uint32_t*>(a + 16 * k);
+          q[k][1] = *reinterpret_cast<const uint32_t*>(c + 16 * k);
+          q[k][2] = *reinterpret_cast<const uint32_t*>(a + 16 * k + 8);
+          q[k][3] = *reinterpret_cast<const uint32_t*>(c + 16 * k + 8);
         }
       }
-      // keys that the rows see (a row past `rows` sees what the last token sees: finite, never stored)
-      const int lim0 = seg.L - p.Lq + min(row0 / p.G, p.Lq - 1) + 1;
-      const int lim1 = seg.L - p.Lq + min(row1 / p.G, p.Lq - 1) + 1;
+      const int lim0 = seg.L - less0, lim1 = seg.L - less1;     // keys that the rows see
       float o[kD / 8][4];
 #pragma unroll
       for (int n = 0; n < kD / 8; ++n)
@@ -452,30 +455,22 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
       if (part == 0) {
         if (whole) {
           const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-          auto dst = [&](int r) {
-            return static_cast<T*>(p.out) + (((int64_t)seg.b * p.Lq + r / p.G) * p.Hq + seg.h * p.G + r % p.G) * kD + 2 * t4;
-          };
-          if (row0 < rows) {
-            T* d = dst(row0);
+          T* d0 = static_cast<T*>(p.out) + item + off0;
+          T* d1 = static_cast<T*>(p.out) + item + off1;
 #pragma unroll
-            for (int n = 0; n < kD / 8; ++n)
-              *reinterpret_cast<uint32_t*>(d + 8 * n) = Pack<T>::of(o[n][0] * i0, o[n][1] * i0);
-          }
-          if (row1 < rows) {
-            T* d = dst(row1);
-#pragma unroll
-            for (int n = 0; n < kD / 8; ++n)
-              *reinterpret_cast<uint32_t*>(d + 8 * n) = Pack<T>::of(o[n][2] * i1, o[n][3] * i1);
+          for (int n = 0; n < kD / 8; ++n) {
+            if (real0) *reinterpret_cast<uint32_t*>(d0 + 8 * n) = Pack<T>::of(o[n][0] * i0, o[n][1] * i0);
+            if (real1) *reinterpret_cast<uint32_t*>(d1 + 8 * n) = Pack<T>::of(o[n][2] * i1, o[n][3] * i1);
           }
         } else {
           const int64_t slot = (2 * (int64_t)w + (first ? 1 : 0)) * rows;
-          if (row0 < rows) {
+          if (real0) {
             float* d = p.o_part + (slot + row0) * kD + 2 * t4;
 #pragma unroll
             for (int n = 0; n < kD / 8; ++n) *reinterpret_cast<float2*>(d + 8 * n) = make_float2(o[n][0], o[n][1]);
             if (t4 == 0) p.ml_part[slot + row0] = make_float2(m0, l0);
           }
-          if (row1 < rows) {
+          if (real1) {
             float* d = p.o_part + (slot + row1) * kD + 2 * t4;
 #pragma unroll
             for (int n = 0; n < kD / 8; ++n) *reinterpret_cast<float2*>(d + 8 * n) = make_float2(o[n][2], o[n][3]);
@@ -514,8 +509,8 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(GqaParams p, int
   constexpr int E = kD / 32;                 // kAhead: parts whose loads are in flight
   __shared__ float so[8][kD];
   __shared__ float sm[8], sl[8];
-  ptx::grid_launch_dependents();
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rows = p.G * p.Lq, share = 8 / per;
   const int row = blockIdx.y * per + warp / share, first = warp % share;

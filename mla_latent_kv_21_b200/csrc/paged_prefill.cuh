@@ -152,9 +152,9 @@ constexpr int kOrderBuckets = 8192;
 __global__ void __launch_bounds__(kOrderThreads) gqa_prefill_order_kernel(GqaParams p) {
   __shared__ int32_t bucket[kOrderBuckets];
   __shared__ int32_t warp_sum[32];
-  ptx::grid_launch_dependents();
   for (int i = threadIdx.x; i < kOrderBuckets; i += kOrderThreads) bucket[i] = 0;
   ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tokens = 2 * (kTile / p.G);
@@ -264,8 +264,11 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   const uint32_t tbase = *tslot;
   constexpr uint32_t kTmemO = 256;       // S (and P) of tile i: columns [128 i, +128); O: [256 + d i, +d)
   bool ok = true;
-  grid_launch_dependents();   // the next grid's blocks may be placed; each waits for this grid
+  // Every access waits for the grid before this one; only then may the next
+  // grid's blocks be placed, so that what they read ahead of their own wait
+  // (weights) is past whatever wrote it.
   grid_dependency_wait();
+  grid_launch_dependents();
 
   // Every role walks the same items in the same order. Barriers are used in
   // phases that each role counts for itself: `items` so far, ring copies, and per

@@ -162,7 +162,8 @@ class GqaAppend(_Bound):
 
 class LatentAppend(_Bound):
     """Appends latent rows to the cache of a DecodePlan with the same dims (bf16, fp32 or FP8) and rotates the RoPE
-    key and the queries' RoPE parts on the way (mla_latent_append)."""
+    key and the queries' RoPE parts on the way (mla_latent_append). Clear a fresh pool once: the latent decode needs
+    the unused slots of a page finite."""
 
     def __init__(self, dims: L.mla_dims_t, rope_style: str = "half"):
         self.dims = dims

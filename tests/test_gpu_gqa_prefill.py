@@ -231,25 +231,32 @@ def test_offsets_past_32_bits(cuda_device):
     _check(out, q, cu, seqs, d, "bf16", "far pages")
 
 
-def test_capture_replay_and_another_stream(cuda_device):
-    new, lens = [300, 20], [300, 500]
-    dev, q, cu, seqs = _inputs(new, lens, 2, 4, 128, torch.bfloat16, 11, cuda_device)
-    plan = M.GqaPrefillPlan(_dims(2, 4, 128, "bf16"), new).allocate_workspace(cuda_device)
-    out = torch.full_like(dev["q"], float("nan"))
+@pytest.mark.parametrize("new,lens,Hk", [([300, 20], [300, 500], 2), ([900, 1, 1400, 260], [900, 700, 1500, 260], 8)])
+def test_capture_replay_and_another_stream(cuda_device, new, lens, Hk):
+    """One item per block, and items drawn from the sorted list; the replays have other counts and lengths."""
+    dev, q, cu, seqs = _inputs(new, lens, Hk, 4, 128, torch.bfloat16, 11, cuda_device)
+    plan = M.GqaPrefillPlan(_dims(Hk, 4, 128, "bf16"), new).allocate_workspace(cuda_device)
+    other = M.GqaPrefillPlan(_dims(Hk, 4, 128, "bf16"), new).allocate_workspace(cuda_device)
+    out, out2 = torch.full_like(dev["q"], float("nan")), torch.full_like(dev["q"], float("nan"))
     side = torch.cuda.Stream(cuda_device)
     torch.cuda.synchronize(cuda_device)
-    _run(plan, dev, out, stream=side.cuda_stream)
+    for _ in range(5):   # two calls in flight at once
+        _run(plan, dev, out, stream=side.cuda_stream)
+        _run(other, dev, out2)
     torch.cuda.synchronize(cuda_device)
     _check(out, q, cu, seqs, 128, "bf16", "side stream")
+    assert torch.equal(out, out2)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         _run(plan, dev, out)
     for seed in (12, 13):
-        fresh, q, cu, seqs = _inputs(new, lens, 2, 4, 128, torch.bfloat16, seed, cuda_device)
+        counts = list(new) if seed == 12 else [new[0] - 7, *new[1:-1], new[-1] + 3 if len(new) > 2 else new[-1]]
+        fresh, q, cu, seqs = _inputs(counts, lens, Hk, 4, 128, torch.bfloat16, seed, cuda_device, extra_rows=sum(new) - sum(counts))
         for name in dev:
             dev[name].copy_(fresh[name])
         out.fill_(float("nan"))
         g.replay()
         torch.cuda.synchronize(cuda_device)
+        assert plan.read_status() == 0
         _check(out, q, cu, seqs, 128, "bf16", "replay")
     del g
