@@ -147,12 +147,11 @@ __device__ __forceinline__ int32_t steps_to(int64_t ahead, int64_t t) {
 // Sorts the items of a call by their steps, longest first (a counting sort; the
 // order among equals is not fixed and moves no result): p.order[i] = (sequence,
 // pair of tiles), p.order_state = {items drawn, items}.
-constexpr int kOrderThreads = 1024;
-constexpr int kOrderBuckets = 8192;
+constexpr int kOrderThreads = 1024;      // and buckets: items of 1023 steps or more share one
 __global__ void __launch_bounds__(kOrderThreads) gqa_prefill_order_kernel(GqaParams p) {
-  __shared__ int32_t bucket[kOrderBuckets];
+  __shared__ int32_t bucket[kOrderThreads];
   __shared__ int32_t warp_sum[32];
-  for (int i = threadIdx.x; i < kOrderBuckets; i += kOrderThreads) bucket[i] = 0;
+  bucket[threadIdx.x] = 0;
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   __syncthreads();
@@ -164,21 +163,15 @@ __global__ void __launch_bounds__(kOrderThreads) gqa_prefill_order_kernel(GqaPar
       const int64_t ahead = checked_len(p, b, false) - n;
       for (int64_t i = lane; i * tokens < n; i += 32) {
         const int32_t nk = steps_to(ahead, min(n, (i + 1) * tokens));
-        put(kOrderBuckets - 1 - min(nk, kOrderBuckets - 1), b, (int32_t)i);   // long ones first
+        put(kOrderThreads - 1 - min(nk, kOrderThreads - 1), b, (int32_t)i);   // long ones first
       }
     }
   };
   walk(true, [&](int k, int, int) { atomicAdd(bucket + k, 1); });
   __syncthreads();
-  // exclusive prefix sums over the buckets, 8 to a thread
-  constexpr int kPer = kOrderBuckets / kOrderThreads;
-  int32_t mine[kPer], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    mine[i] = sum;
-    sum += bucket[kPer * threadIdx.x + i];
-  }
-  int32_t upto = sum;
+  // exclusive prefix sums over the buckets
+  const int32_t mine = bucket[threadIdx.x];
+  int32_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int32_t x = __shfl_up_sync(0xffffffffu, upto, o);
@@ -186,13 +179,14 @@ __global__ void __launch_bounds__(kOrderThreads) gqa_prefill_order_kernel(GqaPar
   }
   if (lane == 31) warp_sum[warp] = upto;
   __syncthreads();
-  int32_t before = upto - sum, total = 0;
-  for (int i = 0; i < 32; ++i) {
-    if (i < warp) before += warp_sum[i];
-    total += warp_sum[i];
-  }
+  int32_t sums = warp_sum[lane];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) bucket[kPer * threadIdx.x + i] = before + mine[i];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int32_t x = __shfl_up_sync(0xffffffffu, sums, o);
+    if (lane >= o) sums += x;
+  }
+  const int32_t before = warp ? __shfl_sync(0xffffffffu, sums, warp - 1) : 0, total = __shfl_sync(0xffffffffu, sums, 31);
+  bucket[threadIdx.x] = before + upto - mine;
   __syncthreads();
   walk(false, [&](int k, int b, int i) {
     const int32_t at = atomicAdd(bucket + k, 1);
