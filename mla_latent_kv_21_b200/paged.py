@@ -75,7 +75,7 @@ class _Bound:
         if at != dev:
             raise ValueError(f"the workspace is on device {at}, the tensors on device {dev}")
         if stream is None:
-            stream = torch.cuda.current_stream(dev).cuda_stream
+            stream = torch._C._cuda_getCurrentRawStream(dev)   # torch.cuda.current_stream(dev) costs a microsecond more
         if dev == torch.cuda.current_device():
             call(*args, workspace, self.workspace_bytes, stream)
         else:
@@ -83,25 +83,29 @@ class _Bound:
                 call(*args, workspace, self.workspace_bytes, stream)
 
 
-def _shapes(args) -> None:
-    """(name, tensor, dtype, shape) of every argument. The C ABI sees bare pointers, so a mismatch is caught here."""
-    for name, t, dtype, shape in args:
+def _check(dev: int, sources, dense) -> None:
+    """(name, tensor, dtype, shape) of every argument: `dense` contiguous, `sources` views whose last dimension is; all
+    on device `dev`. The C ABI sees bare pointers, so a mismatch is caught here."""
+    ok = dev >= 0
+    for _, t, dtype, shape in dense:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+            ok = False
+    for _, t, dtype, shape in sources:
+        if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or (t.stride()[-1] != 1 and t.numel()):
+            ok = False
+    if ok:
+        return
+    for name, t, dtype, shape in (*sources, *dense):
         if t.dtype != dtype or t.shape != shape:
             raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, needed: {dtype} {tuple(shape)}")
-
-
-def _placed(dev: int, sources, dense) -> None:
-    """sources: views whose last dimension is contiguous; dense: contiguous tensors; all on device `dev`."""
     for name, t, _, _ in dense:
-        if t.get_device() != dev or dev < 0 or not t.is_contiguous():
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError(f"{name} must be a contiguous CUDA tensor")
-            raise ValueError(f"{name} is on {t.device}, other tensors on device {dev}")
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous CUDA tensor")
     for name, t, _, _ in sources:
-        if t.get_device() != dev or dev < 0 or (t.stride(-1) != 1 and t.numel()):
-            if not t.is_cuda or t.stride(-1) != 1:
-                raise ValueError(f"{name} must be a CUDA tensor with a contiguous last dimension")
-            raise ValueError(f"{name} is on {t.device}, other tensors on device {dev}")
+        if not t.is_cuda or t.stride(-1) != 1:
+            raise ValueError(f"{name} must be a CUDA tensor with a contiguous last dimension")
+    names = ", ".join(f"{name} on {t.device}" for name, t, _, _ in (*sources, *dense))
+    raise ValueError(f"the tensors are not on one device: {names}")
 
 
 def _act(code):
@@ -116,6 +120,7 @@ class GqaAppend(_Bound):
     def __init__(self, dims: L.mla_gqa_dims_t):
         self.dims = dims
         self._dtype = _act(dims.dtype)
+        self._sizes = dims.num_q_heads, dims.num_kv_heads, dims.head_dim, dims.rope_dim, dims.page_size
 
     def run(self, k, v, k_pool, v_pool, block_table, seq_lens, rope_table=None, q=None, q_out=None, cu_seqlens=None,
             stream: Optional[int] = None) -> None:
@@ -125,10 +130,11 @@ class GqaAppend(_Bound):
         None: dims.q_len new tokens for every sequence."""
         import torch
         d, act, i32 = self.dims, self._dtype, torch.int32
-        Hq, Hk, hd, D = d.num_q_heads, d.num_kv_heads, d.head_dim, d.rope_dim
-        T, B, pool = k.shape[0], seq_lens.shape[0], (k_pool.shape[0], Hk, d.page_size, hd)
+        Hq, Hk, hd, D, P = self._sizes
+        T, B, pool = k.shape[0], seq_lens.shape[0], (k_pool.shape[0], Hk, P, hd)
+        width = block_table.shape[-1]
         sources = [("k", k, act, (T, Hk, hd)), ("v", v, act, (T, Hk, hd))]
-        dense = [("k_pool", k_pool, act, pool), ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (B, block_table.shape[-1])),
+        dense = [("k_pool", k_pool, act, pool), ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (B, width)),
                  ("seq_lens", seq_lens, i32, (B,))]
         q_args, cu, table, positions = (None, 0, 0, None), None, None, 0
         if (q is None) != (q_out is None):
@@ -136,7 +142,8 @@ class GqaAppend(_Bound):
         if D and rope_table is None:
             raise ValueError("rope_table is needed: the dims rotate")
         if D:
-            dense.append(("rope_table", rope_table, torch.float32, (rope_table.shape[0], D)))
+            positions = rope_table.shape[0]
+            dense.append(("rope_table", rope_table, torch.float32, (positions, D)))
             table = rope_table.data_ptr()
         if cu_seqlens is not None:
             dense.append(("cu_seqlens", cu_seqlens, i32, (B + 1,)))
@@ -144,19 +151,15 @@ class GqaAppend(_Bound):
         if q is not None:
             sources.append(("q", q, act, (T, Hq, hd)))
             dense.append(("q_out", q_out, act, (T, Hq, hd)))
-        _shapes(sources)
-        _shapes(dense)
+        dev = k.get_device()
         if cu is None and T != B * d.q_len:
             raise ValueError(f"k: {T} tokens, needed without cu_seqlens: {B} x {d.q_len}")
-        dev = k.get_device()
-        _placed(dev, sources, dense)
+        _check(dev, sources, dense)
         if q is not None:
             q_args = (q.data_ptr(), *q.stride()[:2], q_out.data_ptr())
-        if D:
-            positions = rope_table.shape[0]
         args = L.mla_gqa_append_args_t(k.data_ptr(), *k.stride()[:2], v.data_ptr(), *v.stride()[:2], *q_args,
-                                       k_pool.data_ptr(), v_pool.data_ptr(), pool[0], block_table.data_ptr(),
-                                       block_table.shape[1], B, seq_lens.data_ptr(), cu, T, table, positions)
+                                       k_pool.data_ptr(), v_pool.data_ptr(), pool[0], block_table.data_ptr(), width, B,
+                                       seq_lens.data_ptr(), cu, T, table, positions)
         self._launch(dev, stream, L.mla_gqa_append, d, args)
 
 
@@ -200,9 +203,9 @@ class LatentAppend(_Bound):
         import torch
         d, act, i32 = self.dims, self._dtype, torch.int32
         H, r, D = d.num_heads, d.latent_rank, d.rope_dim
-        T, B = ckv.shape[0], seq_lens.shape[0]
+        T, B, width = ckv.shape[0], seq_lens.shape[0], block_table.shape[-1]
         sources = [("ckv", ckv, act, (T, r))]
-        dense = [*pools, ("block_table", block_table, i32, (B, block_table.shape[-1])), ("seq_lens", seq_lens, i32, (B,))]
+        dense = [*pools, ("block_table", block_table, i32, (B, width)), ("seq_lens", seq_lens, i32, (B,))]
         if (q_rope is None) != (q_rope_out is None):
             raise ValueError("q_rope and q_rope_out come together")
         if D and (k_rope is None or rope_table is None):
@@ -217,19 +220,17 @@ class LatentAppend(_Bound):
             dense.append(("kv_rows", kv_rows, act, (T, r + D)))
         if cu_seqlens is not None:
             dense.append(("cu_seqlens", cu_seqlens, i32, (B + 1,)))
-        _shapes(sources)
-        _shapes(dense)
         if cu_seqlens is None and T != B * d.q_len:
             raise ValueError(f"ckv: {T} tokens, needed without cu_seqlens: {B} x {d.q_len}")
         dev = ckv.get_device()
-        _placed(dev, sources, dense)
+        _check(dev, sources, dense)
         at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         key = (k_rope.data_ptr(), k_rope.stride(0)) if D else (None, 0)
         q_args = (None, 0, 0, None) if q_rope is None else (q_rope.data_ptr(), *q_rope.stride()[:2], q_rope_out.data_ptr())
         out = [t.data_ptr() for _, t, _, _ in pools] + [None] * (3 - len(pools))
         table = (rope_table.data_ptr(), rope_table.shape[0]) if D else (None, 0)
         args = L.mla_latent_append_args_t(ckv.data_ptr(), ckv.stride(0), *key, *q_args, *out, at(kv_rows),
-                                          pools[0][1].shape[0], block_table.data_ptr(), block_table.shape[1], B,
+                                          pools[0][3][0], block_table.data_ptr(), width, B,
                                           seq_lens.data_ptr(), at(cu_seqlens), T, *table)
         self._launch(dev, stream, L.mla_latent_append, d, self.style, args)
 
@@ -240,19 +241,18 @@ class _GqaPlan(_Bound):
     handle = None
     _destroy = None
 
-    def _attend(self, run, stream, shape, q, out, k_pool, v_pool, block_table, lengths):
-        """The checks and the call; lengths: the int32 tensors by (name, tensor, extent), in the call's order."""
+    def _attend(self, run, stream, q, out, k_pool, v_pool, block_table, *lengths):
+        """The checks and the call; lengths: (name, tensor, dtype, shape) in the call's order."""
         import torch
-        d, act, i32 = self.dims, self._dtype, torch.int32
-        pool = (k_pool.shape[0], d.num_kv_heads, d.page_size, d.head_dim)
-        args = [("q", q, act, shape), ("out", out, act, shape), ("k_pool", k_pool, act, pool),
-                ("v_pool", v_pool, act, pool), ("block_table", block_table, i32, (self.batch, block_table.shape[-1])),
-                *[(name, t, i32, (n,)) for name, t, n in lengths]]
-        _shapes(args)
+        act = self._dtype
+        blocks, width = k_pool.shape[0], block_table.shape[-1]
+        pool = (blocks, *self._page)
         dev = q.get_device()
-        _placed(dev, (), args)
-        self._launch(dev, stream, run, self.handle, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), pool[0],
-                     block_table.data_ptr(), block_table.shape[1], *[t.data_ptr() for _, t, _ in lengths], out.data_ptr())
+        _check(dev, (), (("q", q, act, self._rows), ("out", out, act, self._rows), ("k_pool", k_pool, act, pool),
+                         ("v_pool", v_pool, act, pool), ("block_table", block_table, torch.int32, (self.batch, width)),
+                         *lengths))
+        self._launch(dev, stream, run, self.handle, q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), blocks,
+                     block_table.data_ptr(), width, *[x[1].data_ptr() for x in lengths], out.data_ptr())
 
     def close(self) -> None:
         if self.handle:
@@ -276,14 +276,16 @@ class GqaDecodePlan(_GqaPlan):
         self.dims = dims
         self.batch = len(seq_lens_host)
         self._dtype = _act(dims.dtype)
+        self._rows = self.batch, dims.q_len, dims.num_q_heads, dims.head_dim
+        self._page = dims.num_kv_heads, dims.page_size, dims.head_dim
         self.handle, self.workspace_bytes = L.mla_gqa_decode_plan(dims, list(seq_lens_host), num_sms, num_workers)
 
     def run(self, q, k_pool, v_pool, block_table, seq_lens, out, stream: Optional[int] = None) -> None:
         """q, out [B, Lq, Hq, d]; k_pool, v_pool [num_blocks, Hk, 64, d]; block_table int32 [B, *]; seq_lens int32 [B],
         the Lq queries' tokens counted: contiguous CUDA tensors."""
-        d = self.dims
-        self._attend(L.mla_gqa_decode_run, stream, (self.batch, d.q_len, d.num_q_heads, d.head_dim), q, out, k_pool, v_pool,
-                     block_table, (("seq_lens", seq_lens, self.batch),))
+        import torch
+        self._attend(L.mla_gqa_decode_run, stream, q, out, k_pool, v_pool, block_table,
+                     ("seq_lens", seq_lens, torch.int32, (self.batch,)))
 
 
 class GqaPrefillPlan(_GqaPlan):
@@ -297,11 +299,13 @@ class GqaPrefillPlan(_GqaPlan):
         self.new_tokens = [int(x) for x in new_tokens_host]
         self.batch, self.tokens = len(self.new_tokens), sum(self.new_tokens)
         self._dtype = _act(dims.dtype)
+        self._rows = self.tokens, dims.num_q_heads, dims.head_dim
+        self._page = dims.num_kv_heads, dims.page_size, dims.head_dim
         self.handle, self.workspace_bytes = L.mla_gqa_prefill_plan(dims, self.new_tokens)
 
     def run(self, q, k_pool, v_pool, block_table, cu_seqlens, seq_lens, out, stream: Optional[int] = None) -> None:
         """q, out [T, Hq, d] packed; k_pool, v_pool [num_blocks, Hk, 64, d]; block_table int32 [B, *]; cu_seqlens int32
         [B + 1], the prefix sums of the new tokens; seq_lens int32 [B], all tokens: contiguous CUDA tensors."""
-        d = self.dims
-        self._attend(L.mla_gqa_prefill_run, stream, (self.tokens, d.num_q_heads, d.head_dim), q, out, k_pool, v_pool,
-                     block_table, (("cu_seqlens", cu_seqlens, self.batch + 1), ("seq_lens", seq_lens, self.batch)))
+        import torch
+        self._attend(L.mla_gqa_prefill_run, stream, q, out, k_pool, v_pool, block_table,
+                     ("cu_seqlens", cu_seqlens, torch.int32, (self.batch + 1,)), ("seq_lens", seq_lens, torch.int32, (self.batch,)))
