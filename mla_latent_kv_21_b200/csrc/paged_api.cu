@@ -135,7 +135,7 @@ mla_status_t mla_latent_append(const mla_dims_t* dims, int32_t rope_style, const
   if (d.dtype != MLA_BF16 && d.dtype != MLA_FP32 && d.dtype != MLA_FP8_CACHE) return MLA_ERR_INVALID_ARG;
   const bool fp8 = d.dtype == MLA_FP8_CACHE;
   if (d.page_size != 64 || d.rope_dim % 2 != 0 || d.latent_rank > 512 || d.latent_rank + d.rope_dim > 576 ||
-      d.num_heads > 4096 || (fp8 && (d.latent_rank != 512 || d.rope_dim != 64)))
+      d.num_heads > 4096 || (fp8 && (d.latent_rank % 16 != 0 || d.rope_dim % 16 != 0)))
     return MLA_ERR_UNSUPPORTED;
   if (workspace_bytes < kHeaderBytes) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (a.batch < 1 || a.num_tokens < 0 || a.num_blocks < 1 || a.block_table_stride < 1 || a.rope_positions < 0)
@@ -144,7 +144,7 @@ mla_status_t mla_latent_append(const mla_dims_t* dims, int32_t rope_style, const
   if (a.num_tokens == 0) return MLA_OK;
   const bool rot = d.rope_dim > 0;
   if (!a.ckv || !a.kv_pool || !a.block_table || !a.seq_lens || (rot && (!a.k_rope || !a.rope_table)) ||
-      (a.q_rope && (!rot || !a.q_rope_out)) || (fp8 && (!a.kv_rope || !a.kv_scale)))
+      (a.q_rope && (!rot || !a.q_rope_out)) || (fp8 && ((rot && !a.kv_rope) || !a.kv_scale)))
     return MLA_ERR_INVALID_ARG;
   if (!aligned16(a.rope_table)) return MLA_ERR_INVALID_ARG;
   const int V = d.dtype == MLA_FP32 ? 4 : 8;

@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendPar
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int e = kFp8 ? 16 * lane + V * i : V * (lane + 32 * i);
-    if (e < p.r) v[i] = *reinterpret_cast<const uint4*>(c + e);
+    v[i] = e < p.r ? *reinterpret_cast<const uint4*>(c + e) : make_uint4(0, 0, 0, 0);
   }
   const Place at = place_of(p, cs, cu_shared, t, lane == 0);
   if (at.pos < 0) return;
@@ -385,7 +385,8 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendPar
     for (int i = 0; i < 4; ++i)
       w[i] = ptx::cvt_e4m3x2(__fdiv_rn(x[4 * i], scale), __fdiv_rn(x[4 * i + 1], scale)) |
              ptx::cvt_e4m3x2(__fdiv_rn(x[4 * i + 2], scale), __fdiv_rn(x[4 * i + 3], scale)) << 16;
-    *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.k_pool) + cell * p.r + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (16 * lane < p.r)
+      *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.k_pool) + cell * p.r + 16 * lane) = make_uint4(w[0], w[1], w[2], w[3]);
     if (lane == 0) p.kv_scale[cell] = scale;
   }
   for (int u = lane; u < p.D / (2 * V); u += 32) {

@@ -9,11 +9,10 @@
 // items lie on one line (sequence by sequence, head by head), each item behind
 // kItemCost empty places that stand for what a segment costs beside its pages.
 // The line is cut into W equal ranges, one per worker (a block; two share an
-// SM). A range is walked
-// page by page with one pass of a running maximum and sum. An item that lies
-// inside one range is finished there; of the others each range writes its
-// part's maximum, sum and accumulator in fp32, and a second kernel joins the
-// parts of an item in page order.
+// SM). A range is walked page by page with one pass of a running maximum and
+// sum. An item that lies inside one range is finished there; of the others each
+// range writes its part's maximum, sum and accumulator in fp32, and a second
+// kernel joins the parts of an item in page order.
 //
 // A worker is a producer warp, which copies pages by TMA into a ring of key and
 // value slots, and four consumer warps on mma.sync (m16n8k16): with at most 64
@@ -21,7 +20,15 @@
 // hold, and the fragments stay in registers from the scores to the weighted
 // sum. MT = 1, 2 or 4 tiles of 16 rows; 4 / MT warps share a tile and take
 // 16 MT keys of each page, with their own running maximum and sum, joined when
-// the segment ends. Measured: see the launch code.
+// the segment ends.
+//
+// Measured on one B200 (graph replay): 16 x 8192 tokens, 32 heads of their own,
+// 2147.7 MB in 327 us (6.57 TB/s, the copy rate); 1 x 131071 tokens, 64 / 4 heads,
+// 53 us (5.1 TB/s); 64 x 500, 32 / 8 heads, 30 us (4.4 TB/s); one page 4.3 us. A
+// segment's fixed part is about 4400 cycles (queries 500, joining the warps 1700,
+// storing 400, and the latency of one page's scores, weights and sums), most of it
+// instruction fetch; loading the next segment's queries early, joining by column
+// shares of all four warps, and both, changed no case by more than 2%.
 #pragma once
 
 #include "paged_common.cuh"
