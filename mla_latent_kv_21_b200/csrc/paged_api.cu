@@ -54,9 +54,10 @@ bool sm_count(int32_t* out) {
 }
 
 // A failed launch leaves no error behind for a later call to find.
-mla_status_t launched(cudaError_t e = cudaSuccess) {
-  const cudaError_t last = cudaGetLastError();
-  return e == cudaSuccess && last == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+mla_status_t launched(cudaError_t e) {
+  if (e == cudaSuccess) return MLA_OK;
+  (void)cudaGetLastError();
+  return MLA_ERR_CUDA;
 }
 
 // Heads that a thread of an append walks, over token blocks x head blocks of 128

@@ -35,8 +35,12 @@
 // no faster: the maximum found beside the first weights, with those made again
 // where it moves (3370 cycles); for d = 64, weights in columns of their own, so
 // that S(j + 1) is computed during the softmax of step j (3700 cycles: the two
-// tiles fall into step and share the special-function unit); a quarter or half of
-// the exponentials by a polynomial (more instructions, more power).
+// tiles fall into step and share the special-function unit; 3320 when started half
+// a step apart); a quarter or half of the exponentials by a polynomial, and bf16
+// rounding by integer instructions, alone and together (up to 10% slower at
+// d = 128, within the power cap's noise at d = 64). The products themselves run at
+// the tensor core's rate when issued back to back (64 cycles per 128 x 128 x 16
+// from either operand form), also beside tensor-memory loads and exponentials.
 #pragma once
 
 #include "paged_common.cuh"

@@ -56,6 +56,8 @@ class _Bound:
     def read_status(self, stream: Optional[int] = None) -> int:
         """The first error the device recorded since the last call (an mla_status_t), cleared; synchronises."""
         import torch
+        if self.workspace is None:
+            return L.MLA_OK     # nothing has run
         with torch.cuda.device(self.workspace.device):
             if stream is None:
                 stream = torch.cuda.current_stream().cuda_stream

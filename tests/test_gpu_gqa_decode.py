@@ -207,3 +207,37 @@ def test_first_run_inside_a_capture_is_refused_without_a_workspace(cuda_device):
     del g
     _run(plan, dev, out)      # outside of a capture it is allocated on the way
     assert plan.read_status() == 0
+
+
+def test_sequences_that_share_pages(cuda_device):
+    """Two sequences with the same prefix pages, and the same sequence twice."""
+    lens = [300, 200, 300]
+    dev, q, seqs = _inputs(lens, 2, 4, 128, 1, torch.bfloat16, 15, cuda_device)
+    dev["bt"][1, :2] = dev["bt"][0, :2]
+    dev["bt"][2] = dev["bt"][0]
+    k, v = (torch.cat([a[:128], b[128:]]) for a, b in zip(seqs[0], seqs[1]))
+    plan = M.GqaDecodePlan(_dims(2, 4, 128, 1, "bf16"), lens).allocate_workspace(cuda_device)
+    out = torch.full_like(dev["q"], float("nan"))
+    _run(plan, dev, out)
+    assert plan.read_status() == 0
+    _check(out, q, [seqs[0], (k, v), seqs[0]], 128, "bf16", "shared pages")
+
+
+def test_binding_refuses_mixed_devices_and_strided_tensors(cuda_device):
+    lens = [300, 200]
+    dev, _, _ = _inputs(lens, 2, 4, 128, 1, torch.bfloat16, 16, cuda_device)
+    plan = M.GqaDecodePlan(_dims(2, 4, 128, 1, "bf16"), lens)
+    assert plan.read_status() == 0
+    out = torch.zeros_like(dev["q"])
+    for name in ("q", "kp", "vp", "bt", "sl"):
+        with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+            _run(plan, dict(dev, **{name: dev[name].cpu()}), out)
+        wide = torch.stack([dev[name], dev[name]], dim=-1)[..., 0]
+        with pytest.raises(ValueError, match="contiguous CUDA tensor"):
+            _run(plan, dict(dev, **{name: wide}), out)
+    with pytest.raises(ValueError, match="out must be a contiguous CUDA tensor"):
+        _run(plan, dev, out.cpu())
+    assert plan.workspace is None and (out == 0).all()
+    plan.close()
+    with pytest.raises(M.MlaError):      # a closed plan
+        _run(plan, dev, out)
