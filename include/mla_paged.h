@@ -126,7 +126,7 @@ typedef struct {
 
 /* Appends to the latent cache of a decode plan with the same dims (num_heads,
  * latent_rank, rope_dim, q_len and dtype are used): bf16, fp32, or the FP8
- * cache (r and D multiples of 16), where a token's scale is
+ * cache (r and D multiples of 16, D <= 256), where a token's scale is
  *   s = max(max_i |cKV_i| / 448, 2^-64),
  * its codes are e4m3(cKV / s) (round to nearest even) and its RoPE key is
  * stored as bf16(k_rope / s). Only the tokens' own slots are written: clear a

@@ -152,36 +152,37 @@ template <typename T> struct Unit {
   }
 };
 
-// One thread's unit of the heads h0 to h1 - 1 of one token, four heads' loads
-// at a time and the next four under way while a batch is turned and stored.
+// One thread's unit of every step-th head from h0 to h1 - 1 of one token, four
+// heads' loads at a time and the next four under way while a batch is turned and
+// stored.
 // place(): where the token goes and its angles, false if it goes nowhere; it is
 // called with the first loads in flight, since its chain of dependent reads
 // (prefix sums, length, block, table row) is as long as theirs.
 template <typename T, typename Src, typename Place, typename Dst>
-__device__ __forceinline__ void walk_heads(Unit<T>& unit, int h0, int h1, int turned, Src src, Place place, Dst dst) {
+__device__ __forceinline__ void walk_heads(Unit<T>& unit, int h0, int h1, int step, int turned, Src src, Place place, Dst dst) {
   uint4 a[4], b[4];
   auto load = [&](int hb) {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (hb + j < h1) {
-        const T* x = src(hb + j);
+      if (hb + j * step < h1) {
+        const T* x = src(hb + j * step);
         a[j] = *reinterpret_cast<const uint4*>(x + unit.at0);
         b[j] = *reinterpret_cast<const uint4*>(x + unit.at1);
       }
   };
   load(h0);
   if (!place()) return;
-  for (int hb = h0; hb < h1; hb += 4) {
+  for (int hb = h0; hb < h1; hb += 4 * step) {
     uint4 x[4], y[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       x[j] = a[j];
       y[j] = b[j];
     }
-    if (hb + 4 < h1) load(hb + 4);
+    if (hb + 4 * step < h1) load(hb + 4 * step);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int h = hb + j;
+      const int h = hb + j * step;
       if (h < h1) {
         if (unit.turn && h < turned) {
           float x0[Unit<T>::V], x1[Unit<T>::V];
@@ -199,11 +200,17 @@ __device__ __forceinline__ void walk_heads(Unit<T>& unit, int h0, int h1, int tu
   }
 }
 
+// The threads of a block: units x `lanes` heads x tokens. Measured with 1 / 2 / 4 /
+// 8 lanes (heads of a token read by neighbouring threads): latent append of 16K
+// tokens with 128 query heads 115 / 112 / 111 / 107 us (its queries are pieces of
+// 128 bytes), grouped-head append of 14K tokens 51.6 / 52.2 / 53.6 / 63 us (pieces of
+// 256 bytes, and each block has fewer tokens for its one look at the prefix sums).
 constexpr int kAppendThreads = 128;
+constexpr int kGqaLanes = 1, kLatentLanes = 8;
 
 // ----------------------------------------------------- grouped-head cache ----
-// Block (x, y): 128 / (d / 16) tokens x d / 16 units, heads [y * heads_per_cta,
-// ..) of the list q heads, k heads, v heads.
+// Block (x, y): tokens, and heads [y * heads_per_cta, ..) of the list q heads, k
+// heads, v heads.
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads) gqa_append_kernel(AppendParams p, int half_style) {
   __shared__ int32_t cu_shared[kCuShared + 1];
@@ -218,21 +225,21 @@ __global__ void __launch_bounds__(kAppendThreads) gqa_append_kernel(AppendParams
     __syncthreads();
   }
   const int units = p.d / 16;
-  const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / units) + threadIdx.x / units;
+  const int64_t t = (int64_t)blockIdx.x * (kAppendThreads / (units * kGqaLanes)) + threadIdx.x / (units * kGqaLanes);
   if (t >= p.T) return;
   Unit<T> unit(threadIdx.x % units, p.D, half_style != 0);
   const int nq = p.q ? p.Hq : 0, H = nq + 2 * p.Hk;
-  const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(H, h0 + p.heads_per_cta);
+  const int h0 = blockIdx.y * p.heads_per_cta, h1 = min(H, h0 + p.heads_per_cta), lane = threadIdx.x / units % kGqaLanes;
   Place at;
   walk_heads<T>(
-      unit, h0, h1, nq + p.Hk,
+      unit, h0 + lane, h1, kGqaLanes, nq + p.Hk,
       [&](int h) {
         return h < nq ? static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs
              : h < nq + p.Hk ? static_cast<const T*>(p.k) + t * p.k_ts + (h - nq) * p.k_hs
                              : static_cast<const T*>(p.v) + t * p.v_ts + (h - nq - p.Hk) * p.v_hs;
       },
       [&]() {
-        at = place_of(p, cs, cu_shared, t, unit.u == 0 && blockIdx.y == 0);
+        at = place_of(p, cs, cu_shared, t, unit.u == 0 && lane == 0 && blockIdx.y == 0);
         if (at.pos >= 0) unit.angles(p.table + at.pos * p.D, p.D);
         return at.pos >= 0;
       },
@@ -307,8 +314,7 @@ __global__ void __launch_bounds__(kNarrowThreads) latent_append_narrow_kernel(Ap
 }
 
 // Wide path. The first blocks write the latent rows, a warp per token; the
-// others turn the query heads as the grouped-head append does, 128 / (D / 2 V)
-// tokens and heads_per_cta heads to a block.
+// others turn the query heads as the grouped-head append does.
 template <typename T, bool kFp8>
 __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendParams p, int half_style) {
   using VT = Vec<T>;
@@ -326,14 +332,14 @@ __global__ void __launch_bounds__(kAppendThreads) latent_append_kernel(AppendPar
   }
   const int64_t row_blocks = (p.T + 3) / 4;
   if (blockIdx.x >= row_blocks) {
-    const int units = p.D / (2 * V), tokens = kAppendThreads / units;
+    const int units = p.D / (2 * V), tokens = kAppendThreads / (units * kLatentLanes);
     const int64_t token_blocks = (p.T + tokens - 1) / tokens, i = blockIdx.x - row_blocks;
-    const int64_t t = i % token_blocks * tokens + threadIdx.x / units;
-    if (t >= p.T || (int)threadIdx.x >= tokens * units) return;
+    const int64_t t = i % token_blocks * tokens + threadIdx.x / (units * kLatentLanes);
+    if (t >= p.T || (int)threadIdx.x >= tokens * units * kLatentLanes) return;
     Unit<T> unit(threadIdx.x % units, p.D, half_style != 0);
     const int h0 = (int)(i / token_blocks) * p.heads_per_cta, h1 = min(p.Hq, h0 + p.heads_per_cta);
     walk_heads<T>(
-        unit, h0, h1, h1, [&](int h) { return static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs; },
+        unit, h0 + (int)threadIdx.x / units % kLatentLanes, h1, kLatentLanes, h1, [&](int h) { return static_cast<const T*>(p.q) + t * p.q_ts + h * p.q_hs; },
         [&]() {
           const Place at = place_of(p, cs, cu_shared, t, false);   // told by the latent row's warp
           if (at.pos >= 0) unit.angles(p.table + at.pos * p.D, p.D);

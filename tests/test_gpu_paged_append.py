@@ -290,7 +290,7 @@ class Latent:
 
 @pytest.mark.parametrize("style", ["half", "interleaved"])
 @pytest.mark.parametrize("dtype,H,r,D", [("bf16", 128, 512, 64), ("bf16", 16, 256, 64), ("fp32", 8, 64, 16), ("fp32", 4, 512, 64),
-                                         ("fp8", 128, 512, 64), ("fp8", 5, 512, 64), ("fp8", 8, 256, 64), ("fp8", 3, 16, 16), ("fp8", 2, 464, 0), ("bf16", 3, 50, 6), ("fp32", 3, 37, 2),
+                                         ("fp8", 128, 512, 64), ("fp8", 5, 512, 64), ("fp8", 8, 256, 64), ("fp8", 3, 16, 16), ("bf16", 3, 64, 512), ("fp32", 2, 64, 256), ("bf16", 2, 320, 256), ("fp8", 2, 320, 256), ("fp8", 2, 464, 0), ("bf16", 3, 50, 6), ("fp32", 3, 37, 2),
                                          ("bf16", 4, 512, 0), ("fp32", 2, 72, 24)])
 def test_latent_packed(cuda_device, style, dtype, H, r, D):
     c = Latent(COUNTS, H, r, D, dtype, cuda_device, style=style)

@@ -123,7 +123,8 @@ def test_nothing_to_append_is_no_launch():
 @pytest.mark.parametrize("dims,kw,status", [
     (dict(), dict(ckv=None), 1), (dict(), dict(k_rope=None), 1), (dict(), dict(q_rope_out=None), 1), (dict(), dict(rope_table=None), 1),
     (dict(), dict(kv_pool=None), 1), (dict(dtype="fp8"), dict(kv_scale=None), 1), (dict(dtype="fp8"), dict(ckv=(1 << 20) + 2), 1),
-    (dict(dtype="fp8", latent_rank=250), dict(), 2), (dict(dtype="fp8", rope_dim=24), dict(), 2), (dict(rope_dim=63), dict(), 2), (dict(latent_rank=520), dict(), 2),
+    (dict(dtype="fp8", latent_rank=250), dict(), 2), (dict(dtype="fp8", rope_dim=24), dict(), 2),
+    (dict(dtype="fp8", latent_rank=256, rope_dim=272), dict(), 2), (dict(rope_dim=63), dict(), 2), (dict(latent_rank=520), dict(), 2),
     (dict(page_size=16), dict(), 2), (dict(heads=0), dict(), 1), (dict(), dict(cu_seqlens=None), 1), (dict(), dict(num_blocks=0), 1),
 ])
 def test_latent_append_arguments(dims, kw, status):
