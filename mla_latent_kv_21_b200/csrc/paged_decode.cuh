@@ -18,17 +18,22 @@
 // value slots, and four consumer warps on mma.sync (m16n8k16): with at most 64
 // rows of a page the product is far below what a tcgen05 tile (128 rows) would
 // hold, and the fragments stay in registers from the scores to the weighted
-// sum. MT = 1, 2 or 4 tiles of 16 rows; 4 / MT warps share a tile and take
-// 16 MT keys of each page, with their own running maximum and sum, joined when
-// the segment ends.
+// sum. MT = 1, 2 or 4 tiles of 16 rows. With 2 tiles two warps share a tile and
+// take half the keys of each page, with their own running maximum and sum, joined
+// when the segment ends; with 1 tile there are two such pairs, each with half of
+// the output columns (both compute the same scores, 16 more products a page, and
+// the join moves a quarter of what four key parts would). Against four key parts, three
+// runs of each in turn: 256 x 64 tokens 26.2 us instead of 30.3, 1 x 500 7.65 instead
+// of 8.2, 128 x 200 31.1 instead of 32.7, but 16 x 8192 334.4 instead of 330.1 and 32 x
+// 2000 50.9 instead of 50.6: the scores that are computed twice show where the memory
+// is the bound. Four column parts: 363 at 16 x 8192.
 //
 // Measured on one B200 (graph replay): 16 x 8192 tokens, 32 heads of their own,
-// 2147.7 MB in 327 us (6.57 TB/s, the copy rate); 1 x 131071 tokens, 64 / 4 heads,
-// 53 us (5.1 TB/s); 64 x 500, 32 / 8 heads, 30 us (4.4 TB/s); one page 4.3 us. A
-// segment's fixed part is about 4400 cycles (queries 500, joining the warps 1700,
-// storing 400, and the latency of one page's scores, weights and sums), most of it
-// instruction fetch; loading the next segment's queries early, joining by column
-// shares of all four warps, and both, changed no case by more than 2%.
+// 2147.7 MB in 331 to 338 us (6.4 to 6.5 TB/s; the copy rate is 6.55); 1 x 131071
+// tokens, 64 / 4 heads, 53 us (5.0 TB/s); 64 x 500, 32 / 8 heads, 30 us (4.4 TB/s); one page 4.3 us. A
+// segment's fixed part (queries, joining the warps, storing, the latency of one
+// page) is thousands of cycles, most of it instruction fetch: loading the next
+// segment's queries early changed no case by more than 2%.
 #pragma once
 
 #include "paged_common.cuh"
@@ -38,9 +43,12 @@ namespace pg {
 
 constexpr int kDecodeThreads = 160;
 // Loading an item's queries, joining the warps and storing takes a worker about
-// as long as this many pages. Measured at 64 sequences of 1 to 16384 tokens, 8
-// key heads (many items of one page): 111 us with 0, 64.3 with 2, 59.1 with 4, 59.6
-// with 8; no effect where items are long.
+// as long as this many pages. Measured (graph replay, two runs of each in turn) at 64
+// sequences of 1 to 16384 tokens, 8 key heads (many items of one page): 90.5 us with
+// 0, 56.7 with 2, 56.6 with 3, 56.1 with 4, 56.8 with 6; at 128 x 200 tokens 31.5, 30.6,
+// 30.9, 31.1 and 31.3, at 32 x 4000 with 32 rows a key head 97.9, 97.2, 96.8, 97.4 and
+// 98.3: from 2 to 4 it hardly matters. Only one short item is better off with 0 (1 x
+// 500: 6.9 instead of 7.6).
 constexpr int kItemCost = 4;
 
 template <int kD> struct DecodeSmem {
@@ -138,9 +146,11 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   using namespace ptx;
   using S = DecodeSmem<kD>;
   using WS = WeightScale<T>;
-  constexpr int kParts = 4 / MT;           // warps that share a tile of rows
-  constexpr int kKeys = 16 * MT;           // keys of a page per warp
+  constexpr int kHalves = MT == 1 ? 2 : 1;         // warps with the same rows and keys, each with its output columns
+  constexpr int kParts = 4 / (MT * kHalves);       // warps with the same rows and columns, each with its keys
+  constexpr int kKeys = kPage / kParts;            // keys of a page per warp
   constexpr int NT = kKeys / 8;
+  constexpr int kDW = kD / kHalves;                // output columns of a warp
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   const uint32_t base = (raw + 1023u) & ~1023u;
@@ -246,7 +256,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         uint4* o = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (int64_t)b * p.Lq * p.Hq * kD);
         for (int i = threadIdx.x; i < p.Lq * p.Hq * (kD / 8); i += 128) o[i] = make_uint4(0, 0, 0, 0);
       }
-    const int tile = warp % MT, part = warp / MT;
+    const int tile = warp % MT, part = warp / MT % kParts, half = warp / (MT * kParts);
     const int g = lane >> 2, t4 = lane & 3;
     const int row0 = 16 * tile + g, row1 = row0 + 8;
     const int key0 = part * kKeys;           // this warp's first key of a page
@@ -262,7 +272,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
     float* join = reinterpret_cast<float*>(gbase + S::join);
     // shared-memory offsets of this lane's ldmatrix rows
     const uint32_t k_row = key0 + (lane & 7), k_chunk = lane >> 3;
-    const uint32_t v_row = key0 + ((lane >> 3) & 1) * 8 + (lane & 7), v_chunk = lane >> 4;
+    const uint32_t v_row = key0 + ((lane >> 3) & 1) * 8 + (lane & 7), v_chunk = half * (kDW / 8) + (lane >> 4);
     uint32_t it = 0;
     int2 tail = make_int2(-1, 0);
     for (; have; have = seg.next(p)) {
@@ -280,9 +290,9 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         }
       }
       const int lim0 = seg.L - less0, lim1 = seg.L - less1;     // keys that the rows see
-      float o[kD / 8][4];
+      float o[kDW / 8][4];
 #pragma unroll
-      for (int n = 0; n < kD / 8; ++n)
+      for (int n = 0; n < kDW / 8; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
       float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
@@ -346,7 +356,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
           l0 *= a0;
           l1 *= a1;
 #pragma unroll
-          for (int n = 0; n < kD / 8; ++n) {
+          for (int n = 0; n < kDW / 8; ++n) {
             o[n][0] *= a0;
             o[n][1] *= a0;
             o[n][2] *= a1;
@@ -379,7 +389,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
             z1 = (k0 + 8 < keys ? 0x0000ffffu : 0u) | (k0 + 9 < keys ? 0xffff0000u : 0u);
           }
 #pragma unroll
-          for (int n = 0; n < kD / 16; ++n) {
+          for (int n = 0; n < kDW / 16; ++n) {
             const uint32_t chunk = 2 * n + v_chunk;
             uint32_t f[4];
             ldsm4_t(f, vb + (chunk >> 3) * 8192 + r * 128 + (((chunk & 7) ^ (r & 7)) << 4));
@@ -407,21 +417,21 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
         float n0 = -INFINITY, n1 = -INFINITY;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          n0 = fmaxf(n0, sm[16 * (i * MT + tile) + g]);
-          n1 = fmaxf(n1, sm[16 * (i * MT + tile) + g + 8]);
+          n0 = fmaxf(n0, sm[16 * ((half * kParts + i) * MT + tile) + g]);
+          n1 = fmaxf(n1, sm[16 * ((half * kParts + i) * MT + tile) + g + 8]);
         }
         const float a0 = m0 == -INFINITY ? 0.f : ex2_approx(m0 - n0), a1 = m1 == -INFINITY ? 0.f : ex2_approx(m1 - n1);
         l0 = l1 = 0.f;
 #pragma unroll
         for (int i = 0; i < kParts; ++i) {
-          const int x = 16 * (i * MT + tile) + g;
+          const int x = 16 * ((half * kParts + i) * MT + tile) + g;
           if (sm[x] != -INFINITY) l0 += sl[x] * ex2_approx(sm[x] - n0);
           if (sm[x + 8] != -INFINITY) l1 += sl[x + 8] * ex2_approx(sm[x + 8] - n1);
         }
         m0 = n0;
         m1 = n1;
 #pragma unroll
-        for (int n = 0; n < kD / 8; ++n) {
+        for (int n = 0; n < kDW / 8; ++n) {
           o[n][0] *= a0;
           o[n][1] *= a0;
           o[n][2] *= a1;
@@ -434,19 +444,19 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
 #pragma unroll
           for (int i = 1; i < kParts; ++i) {
             named_barrier(1, 128);
-            float* buf = join + tile * (16 * kD / MT) + lane * 4;
+            float* buf = join + (half * MT + tile) * (16 * kDW / MT) + lane * 4;
             if (part == i) {
 #pragma unroll
-              for (int n = 0; n < kD / 8 / MT; ++n)
-                *reinterpret_cast<float4*>(buf + 128 * n) = make_float4(o[c * (kD / 8 / MT) + n][0], o[c * (kD / 8 / MT) + n][1],
-                                                                        o[c * (kD / 8 / MT) + n][2], o[c * (kD / 8 / MT) + n][3]);
+              for (int n = 0; n < kDW / 8 / MT; ++n)
+                *reinterpret_cast<float4*>(buf + 128 * n) = make_float4(o[c * (kDW / 8 / MT) + n][0], o[c * (kDW / 8 / MT) + n][1],
+                                                                        o[c * (kDW / 8 / MT) + n][2], o[c * (kDW / 8 / MT) + n][3]);
             }
             named_barrier(1, 128);
             if (part == 0) {
 #pragma unroll
-              for (int n = 0; n < kD / 8 / MT; ++n) {
+              for (int n = 0; n < kDW / 8 / MT; ++n) {
                 const float4 x = *reinterpret_cast<const float4*>(buf + 128 * n);
-                float(&y)[4] = o[c * (kD / 8 / MT) + n];
+                float(&y)[4] = o[c * (kDW / 8 / MT) + n];
                 y[0] += x.x;
                 y[1] += x.y;
                 y[2] += x.z;
@@ -462,26 +472,26 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
       if (part == 0) {
         if (whole) {
           const float i0 = l0 > 0.f ? 1.f / l0 : 0.f, i1 = l1 > 0.f ? 1.f / l1 : 0.f;
-          T* d0 = static_cast<T*>(p.out) + item + off0;
-          T* d1 = static_cast<T*>(p.out) + item + off1;
+          T* d0 = static_cast<T*>(p.out) + item + off0 + half * kDW;
+          T* d1 = static_cast<T*>(p.out) + item + off1 + half * kDW;
 #pragma unroll
-          for (int n = 0; n < kD / 8; ++n) {
+          for (int n = 0; n < kDW / 8; ++n) {
             if (real0) *reinterpret_cast<uint32_t*>(d0 + 8 * n) = Pack<T>::of(o[n][0] * i0, o[n][1] * i0);
             if (real1) *reinterpret_cast<uint32_t*>(d1 + 8 * n) = Pack<T>::of(o[n][2] * i1, o[n][3] * i1);
           }
         } else {
           const int64_t slot = (2 * (int64_t)w + (first ? 1 : 0)) * rows;
           if (real0) {
-            float* d = p.o_part + (slot + row0) * kD + 2 * t4;
+            float* d = p.o_part + (slot + row0) * kD + half * kDW + 2 * t4;
 #pragma unroll
-            for (int n = 0; n < kD / 8; ++n) *reinterpret_cast<float2*>(d + 8 * n) = make_float2(o[n][0], o[n][1]);
-            if (t4 == 0) p.ml_part[slot + row0] = make_float2(m0, l0);
+            for (int n = 0; n < kDW / 8; ++n) *reinterpret_cast<float2*>(d + 8 * n) = make_float2(o[n][0], o[n][1]);
+            if (t4 == 0 && half == 0) p.ml_part[slot + row0] = make_float2(m0, l0);
           }
           if (real1) {
-            float* d = p.o_part + (slot + row1) * kD + 2 * t4;
+            float* d = p.o_part + (slot + row1) * kD + half * kDW + 2 * t4;
 #pragma unroll
-            for (int n = 0; n < kD / 8; ++n) *reinterpret_cast<float2*>(d + 8 * n) = make_float2(o[n][2], o[n][3]);
-            if (t4 == 0) p.ml_part[slot + row1] = make_float2(m1, l1);
+            for (int n = 0; n < kDW / 8; ++n) *reinterpret_cast<float2*>(d + 8 * n) = make_float2(o[n][2], o[n][3]);
+            if (t4 == 0 && half == 0) p.ml_part[slot + row1] = make_float2(m1, l1);
           }
         }
       }
