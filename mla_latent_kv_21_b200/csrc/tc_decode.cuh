@@ -351,9 +351,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads_of<S>(), 1)
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
   // the setup above overlaps the previous kernel; from here on its results
-  // (the absorbed queries, the page prefix sums) are read
-  grid_launch_dependents();
+  // (the absorbed queries, the page prefix sums) are read. The combine, which
+  // waits for no grid, reads the absorb kernel's results too: it may be placed
+  // only once they are complete, so the trigger stands behind the wait.
   grid_dependency_wait();
+  grid_launch_dependents();
   const bool run = *p.lengths_ok != 0;  // uniform across the pair
   MLA_TRACE_CTA(1);
 

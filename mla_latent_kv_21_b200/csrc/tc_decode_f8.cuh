@@ -207,8 +207,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync_all();
   tc_fence_after();
   const uint32_t tbase = *tmem_slot;
-  grid_launch_dependents();
+  // the combine waits for no grid and reads the absorb kernel's results: the
+  // trigger that lets it start stands behind the wait for them
   grid_dependency_wait();
+  grid_launch_dependents();
   const bool run = *p.lengths_ok != 0;
 
   auto fail = [&](int code) {

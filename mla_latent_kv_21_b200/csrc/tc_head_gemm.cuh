@@ -264,11 +264,12 @@ __global__ void __launch_bounds__(kCombineThreads, 1)
   const uint32_t tbase = *tslot;
   grid_launch_dependents();
   // No grid-wide wait for the decode kernel: this grid starts once every decode
-  // CTA has passed its setup (all of them resident), and each merge item waits
-  // below for its own sequence's segments only, so the sequences that finish
-  // early are merged while the last decode pairs still run. The prefix sums and
-  // the length flag come from the absorb kernel, complete before the decode
-  // kernel started.
+  // CTA (all of them resident) has waited for the absorb kernel, and each merge
+  // item waits below for its own sequence's segments only, so the sequences that
+  // finish early are merged while the last decode pairs still run. The prefix
+  // sums, the length flag and the cleared segment counts come from the absorb
+  // kernel: every decode CTA triggers this grid only behind its own wait, so
+  // they are complete whatever runs ahead of the absorb kernel.
   const bool run = *p.lengths_ok != 0;
   if (run) {
     // ---- merge: one item = one row x 32 latent columns (64 bytes of each fp16
