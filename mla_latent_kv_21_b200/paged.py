@@ -5,7 +5,8 @@ argument checks only; every computation runs inside libmla_decode.so.
 Every run() works on its tensors' device, on `stream` or that device's current
 stream, without synchronising; errors found on the device are read with
 read_status(). An object's workspace serves one call in flight: use one object
-per stream (or per captured graph) that may overlap with another.
+per stream (or per captured graph) that may overlap with another. An object may
+be dropped while its call runs, but not while a graph that captured one lives.
 """
 
 from __future__ import annotations
@@ -13,6 +14,7 @@ from __future__ import annotations
 from typing import Optional, Sequence
 
 from . import _lib as L
+from ._workspace import Workspace
 
 _DTYPES = {"bf16": L.MLA_BF16, "fp16": L.MLA_FP16, "fp32": L.MLA_FP32, "fp8": L.MLA_FP8_CACHE}
 _STYLES = {"half": L.MLA_ROPE_HALF, "interleaved": L.MLA_ROPE_INTERLEAVED}
@@ -34,55 +36,18 @@ def rope_table(positions: int, rope_dim: int, base: float = 10000.0, device="cud
     return torch.cat([ang.cos(), ang.sin()], dim=1).float().to(device)
 
 
-class _Bound:
-    """A workspace, its status word and the checks that the classes share."""
-
-    workspace = None
-    workspace_bytes = 1024
-    _at = -1, 0   # the workspace's device and address
-
-    def allocate_workspace(self, device, stream: Optional[int] = None):
-        """Allocates and clears the workspace on `stream` (default: the device's current stream)."""
-        import torch
-        device = torch.device(device)
-        with torch.cuda.device(device):
-            self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device="cuda")
-            if stream is None:
-                stream = torch.cuda.current_stream().cuda_stream
-            L.mla_workspace_init(self.workspace.data_ptr(), self.workspace_bytes, stream)
-        self._at = self.workspace.get_device(), self.workspace.data_ptr()
-        return self
-
-    def read_status(self, stream: Optional[int] = None) -> int:
-        """The first error the device recorded since the last call (an mla_status_t), cleared; synchronises."""
-        import torch
-        if self.workspace is None:
-            return L.MLA_OK     # nothing has run
-        with torch.cuda.device(self.workspace.device):
-            if stream is None:
-                stream = torch.cuda.current_stream().cuda_stream
-            return L.mla_decode_read_status(self.workspace.data_ptr(), stream)
+class _Bound(Workspace):
+    """A workspace and the launch that the classes share."""
 
     def _launch(self, dev: int, stream, call, *args) -> None:
         """call(*args, workspace, workspace bytes, stream) with device `dev` current."""
         import torch
-        if self.workspace is None:
-            if torch.cuda.is_current_stream_capturing():
-                raise RuntimeError("allocate_workspace() before capturing: memory allocated under a capture belongs "
-                                   "to the graph")
-            self.allocate_workspace(dev)
-            if stream is not None:  # the allocation and its clearing are ordered on the current stream
-                torch.cuda.ExternalStream(stream, device=dev).wait_stream(torch.cuda.current_stream(dev))
-        at, workspace = self._at
-        if at != dev:
-            raise ValueError(f"the workspace is on device {at}, the tensors on device {dev}")
-        if stream is None:
-            stream = torch._C._cuda_getCurrentRawStream(dev)   # torch.cuda.current_stream(dev) costs a microsecond more
+        stream = self._stream(dev, stream)
         if dev == torch.cuda.current_device():
-            call(*args, workspace, self.workspace_bytes, stream)
+            call(*args, self._at[1], self.workspace_bytes, stream)
         else:
             with torch.cuda.device(dev):
-                call(*args, workspace, self.workspace_bytes, stream)
+                call(*args, self._at[1], self.workspace_bytes, stream)
 
 
 def _check(dev: int, sources, dense) -> None:

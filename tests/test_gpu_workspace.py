@@ -1,0 +1,161 @@
+"""Workspaces and streams: a plan dropped while its call runs on another stream
+keeps its memory until the call is done; a stream that uses a workspace waits
+until it is cleared; nothing is allocated for a stream under capture."""
+
+import pytest
+import torch
+
+import mla_latent_kv_21_b200 as M
+
+from harness_paged import block_tables, check_attention, generator, paged_kv
+
+pytestmark = pytest.mark.gpu
+
+LENS, HK, G, D = [700, 64, 0, 2100], 2, 4, 128
+
+
+class Case:
+    """Decode (one query per sequence) and prefill (20 new tokens per sequence) over one cache."""
+
+    def __init__(self, device, seed=1):
+        gen = generator(seed)
+        table, blocks = block_tables(LENS, gen)
+        kp, vp, self.seqs = paged_kv(LENS, HK, D, torch.bfloat16, gen, table, blocks)
+        self.kp, self.vp, self.bt = kp.to(device), vp.to(device), table.to(device)
+        self.sl = torch.tensor(LENS, dtype=torch.int32, device=device)
+        self.dims = M.gqa_dims_for(HK * G, HK, D, D ** -0.5, "bf16")
+        self.q = torch.randn((4, 1, HK * G, D), generator=gen).to(torch.bfloat16).to(device)
+        self.new = [20, 20, 0, 20]
+        self.cu = torch.tensor([0, 20, 40, 40, 60], dtype=torch.int32, device=device)
+        self.qp = torch.randn((60, HK * G, D), generator=gen).to(torch.bfloat16).to(device)
+
+    def make(self, what):
+        return M.GqaDecodePlan(self.dims, LENS) if what == "decode" else M.GqaPrefillPlan(self.dims, self.new)
+
+    def run(self, plan, what, stream=None):
+        q = self.q if what == "decode" else self.qp
+        out = torch.full_like(q, float("nan"))
+        torch.cuda.synchronize()
+        self.launch(plan, what, out, stream)
+        return out
+
+    def launch(self, plan, what, out, stream=None):
+        if what == "decode":
+            plan.run(self.q, self.kp, self.vp, self.bt, self.sl, out, stream=stream)
+        else:
+            plan.run(self.qp, self.kp, self.vp, self.bt, self.cu, self.sl, out, stream=stream)
+
+    def check(self, out, what):
+        for b, (k, v) in enumerate(self.seqs):
+            rows = slice(int(self.cu[b]), int(self.cu[b + 1]))
+            q, o = (self.q[b], out[b]) if what == "decode" else (self.qp[rows], out[rows])
+            check_attention(o, q, k, v, D ** -0.5, torch.bfloat16, f"{what}, sequence {b}")
+
+
+def _keep_busy(stream, device):
+    """Products of about a tenth of a second on `stream`, with tensors that stay alive."""
+    with torch.cuda.stream(stream):
+        a = torch.randn((8192, 8192), device=device, dtype=torch.bfloat16)
+        b = torch.empty_like(a)
+        for _ in range(150):
+            torch.matmul(a, a, out=b)
+    return a, b
+
+
+@pytest.mark.parametrize("what", ["decode", "prefill"])
+def test_a_plan_dropped_while_its_call_waits_on_another_stream(cuda_device, what):
+    c = Case(cuda_device)
+    side = torch.cuda.Stream(cuda_device)
+    c.run(c.make(what), what)         # loads the kernels, which may synchronise
+    _keep_busy(side, cuda_device)
+    out = torch.full_like(c.q if what == "decode" else c.qp, float("nan"))
+    torch.cuda.synchronize()
+    busy = _keep_busy(side, cuda_device)
+    plan = c.make(what)
+    c.launch(plan, what, out, side.cuda_stream)
+    size, at = plan.workspace_bytes, plan.workspace.data_ptr()
+    del plan                          # no cycle holds it: its memory goes back at once
+    assert not side.query()           # the call has not run yet
+    others = [torch.full((size,), 0x5b, dtype=torch.uint8, device=cuda_device) for _ in range(4)]
+    ranges = [(t.data_ptr(), t.data_ptr() + size) for t in others]
+    torch.cuda.synchronize()
+    assert all(at + size <= lo or hi <= at for lo, hi in ranges)
+    c.check(out, what)
+    del busy
+
+
+@pytest.mark.parametrize("what", ["decode", "prefill"])
+def test_a_stream_waits_until_the_workspace_is_cleared(cuda_device, what):
+    """Allocated on the busy current stream, first used on another one; and allocated for another stream directly."""
+    c = Case(cuda_device)
+    side, third = torch.cuda.Stream(cuda_device), torch.cuda.Stream(cuda_device)
+    c.run(c.make(what), what)         # loads the kernels, which may synchronise
+    _keep_busy(torch.cuda.current_stream(), cuda_device)
+    for direct in (False, True):
+        plan = c.make(what)
+        outs = [torch.full_like(c.q if what == "decode" else c.qp, float("nan")) for _ in range(2)]
+        torch.cuda.synchronize()
+        busy = _keep_busy(torch.cuda.current_stream(), cuda_device)
+        if direct:
+            plan.allocate_workspace(cuda_device, stream=side.cuda_stream)
+        else:
+            plan.allocate_workspace(cuda_device)
+        c.launch(plan, what, outs[0], side.cuda_stream)
+        assert not side.query()       # it waits for the current stream's products
+        side.synchronize()
+        c.launch(plan, what, outs[1], third.cuda_stream)
+        torch.cuda.synchronize()
+        assert plan.read_status() == 0
+        for out in outs:
+            c.check(out, what)
+        del busy
+
+
+def test_the_default_stream_by_its_handle(cuda_device):
+    """Handle 0 while another stream is current."""
+    c = Case(cuda_device)
+    plan = c.make("decode")
+    side = torch.cuda.Stream(cuda_device)
+    with torch.cuda.stream(side):
+        out = c.run(plan, "decode", stream=0)
+        assert torch.cuda.default_stream(cuda_device).cuda_stream in plan._streams
+        torch.cuda.synchronize()
+    assert plan.read_status(0) == 0
+    c.check(out, "decode")
+
+
+def test_a_first_run_on_a_capturing_stream_is_refused(cuda_device):
+    """`stream` captures, the current stream does not."""
+    c = Case(cuda_device)
+    side = torch.cuda.Stream(cuda_device)
+    x = torch.zeros(4, device=cuda_device)
+    plan, ready = c.make("decode"), c.make("decode").allocate_workspace(cuda_device)
+    out = torch.full_like(c.q, float("nan"))
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side, capture_error_mode="thread_local"):
+        x += 1
+        with torch.cuda.stream(torch.cuda.default_stream(cuda_device)):
+            with pytest.raises(RuntimeError, match="allocate_workspace"):
+                c.launch(plan, "decode", out, side.cuda_stream)
+            with pytest.raises(RuntimeError, match="before capturing"):
+                plan.allocate_workspace(cuda_device, stream=side.cuda_stream)
+        c.launch(ready, "decode", out, side.cuda_stream)
+    assert plan.workspace is None
+    g.replay()
+    torch.cuda.synchronize()
+    assert ready.read_status() == 0 and (x == 1).all()
+    c.check(out, "decode")
+    out.fill_(float("nan"))
+    c.launch(ready, "decode", out, side.cuda_stream)      # eager after the capture, on the stream that captured
+    torch.cuda.synchronize()
+    c.check(out, "decode")
+    del g
+
+
+def test_a_workspace_on_another_device_is_refused(cuda_device):
+    c = Case(cuda_device)
+    plan = c.make("decode").allocate_workspace(cuda_device)
+    plan._at = 1, plan._at[1]
+    with pytest.raises(ValueError, match="the workspace is on device 1"):
+        c.run(plan, "decode")
