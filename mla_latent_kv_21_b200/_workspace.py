@@ -36,6 +36,7 @@ class Workspace:
     _at = -1, 0          # the workspace's device and address
     _streams = ()        # raw handles that wait for the clearing and are recorded
     _cleared = None      # event behind the clearing
+    _allocates_under_capture = False   # a first run may take its workspace from a graph's own memory
 
     def allocate_workspace(self, device, stream: Optional[int] = None):
         """Allocates and clears the workspace on `stream` (default: the device's current stream)."""
@@ -66,10 +67,12 @@ class Workspace:
         allocated if there is none yet."""
         import torch
         if self.workspace is None:
-            if torch.cuda.is_current_stream_capturing() or (stream is not None and _capturing(stream_of(stream, dev))):
+            capturing = torch.cuda.is_current_stream_capturing() or (
+                stream is not None and _capturing(stream_of(stream, dev)))
+            if capturing and not self._allocates_under_capture:
                 raise RuntimeError("allocate_workspace() before capturing: memory allocated under a capture belongs "
                                    "to the graph")
-            self.allocate_workspace(dev, stream)
+            self.allocate_workspace(dev, None if capturing else stream)
         if self._at[0] != dev:
             raise ValueError(f"the workspace is on device {self._at[0]}, the tensors on device {dev}")
         if stream is None:

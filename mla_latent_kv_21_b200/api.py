@@ -6,6 +6,7 @@ from __future__ import annotations
 from typing import Optional, Sequence
 
 from . import _lib as L
+from ._workspace import Workspace
 
 
 def dims_for(heads: int, latent_rank: int, rope_dim: int, nope_dim: int, v_dim: int,
@@ -16,8 +17,10 @@ def dims_for(heads: int, latent_rank: int, rope_dim: int, nope_dim: int, v_dim: 
                        latent_shards, float(softmax_scale), code)
 
 
-class DecodePlan:
+class DecodePlan(Workspace):
     """Owns one plan handle and (once bound) its device workspace tensor."""
+
+    _allocates_under_capture = True
 
     def __init__(self, dims: L.mla_dims_t, seq_lens_host: Sequence[int], num_sms: int = 0,
                  kernel: int = L.MLA_KERNEL_AUTO, num_workers: int = 0):
@@ -26,14 +29,6 @@ class DecodePlan:
         self.handle, self.workspace_bytes = L.mla_decode_plan_ex(
             dims, list(seq_lens_host), num_sms, kernel, num_workers)
         self.info = L.mla_plan_get_info(self.handle)
-        self.workspace = None
-
-    def allocate_workspace(self, device) -> "DecodePlan":
-        import torch
-        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
-        L.mla_workspace_init(self.workspace.data_ptr(), self.workspace_bytes,
-                             torch.cuda.current_stream(device).cuda_stream)
-        return self
 
     def segments(self):
         return L.mla_plan_segments(self.handle)
@@ -74,10 +69,7 @@ class DecodePlan:
                         ("w_uv", w_uv), ("out", out)):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if self.workspace is None:
-            self.allocate_workspace(q_nope.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(q_nope.device).cuda_stream
+        stream = self._stream(q_nope.get_device(), stream)
         # decode_events: optional (start, stop) raw cudaEvent_t handles (ints)
         ev0, ev1 = (None, None) if decode_events is None else decode_events
         L.mla_decode_run_ex(self.handle, q_nope.data_ptr(), q_rope.data_ptr(),
@@ -103,10 +95,7 @@ class DecodePlan:
                         ("seq_lens", seq_lens), ("w_uk", w_uk), ("w_uv", w_uv), ("out", out)):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if self.workspace is None:
-            self.allocate_workspace(q_nope.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(q_nope.device).cuda_stream
+        stream = self._stream(q_nope.get_device(), stream)
         ev0, ev1 = (None, None) if decode_events is None else decode_events
         L.mla_decode_run_fp8(self.handle, q_nope.data_ptr(), q_rope.data_ptr(), kv_codes.data_ptr(),
                              kv_rope.data_ptr(), kv_scale.data_ptr(), kv_codes.shape[0],
@@ -128,10 +117,7 @@ class DecodePlan:
                         ("w_uv", w_uv), ("out", out)):
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if self.workspace is None:
-            self.allocate_workspace(q_nope.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(q_nope.device).cuda_stream
+        stream = self._stream(q_nope.get_device(), stream)
         ev0, ev1 = (None, None) if decode_events is None else decode_events
         L.mla_decode_run_blasst(self.handle, q_nope.data_ptr(), q_rope.data_ptr(), kv_pool.data_ptr(),
                                 kv_pool.shape[0], block_table.data_ptr(), block_table.shape[1],
@@ -146,12 +132,6 @@ class DecodePlan:
         c = self.workspace[8:16].view(torch.int32).cpu().tolist()
         return c[0], c[1]
 
-    def read_status(self, stream: Optional[int] = None) -> int:
-        import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self.workspace.device).cuda_stream
-        return L.mla_decode_read_status(self.workspace.data_ptr(), stream)
-
     def close(self) -> None:
         if self.handle:
             L.mla_plan_destroy(self.handle)
@@ -164,22 +144,16 @@ class DecodePlan:
             pass
 
 
-class PrefillPlan:
+class PrefillPlan(Workspace):
     """Owns one prefill plan handle and its device workspace tensor (the
     up-projected per-head keys and values)."""
+
+    _allocates_under_capture = True
 
     def __init__(self, dims: L.mla_dims_t, seq_lens_host: Sequence[int]):
         self.dims = dims
         self.lens = [int(x) for x in seq_lens_host]
         self.handle, self.workspace_bytes = L.mla_prefill_plan(dims, self.lens)
-        self.workspace = None
-
-    def allocate_workspace(self, device) -> "PrefillPlan":
-        import torch
-        self.workspace = torch.empty(self.workspace_bytes, dtype=torch.uint8, device=device)
-        L.mla_workspace_init(self.workspace.data_ptr(), self.workspace_bytes,
-                             torch.cuda.current_stream(device).cuda_stream)
-        return self
 
     def run(self, q_nope, q_rope, kv_rows, cu_seqlens, w_uk, w_uv, out, stream: Optional[int] = None,
             attn_events=None) -> None:
@@ -198,20 +172,11 @@ class PrefillPlan:
                 raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)}, the plan needs {dtype} {shape}")
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous CUDA tensor")
-        if self.workspace is None:
-            self.allocate_workspace(q_nope.device)
-        if stream is None:
-            stream = torch.cuda.current_stream(q_nope.device).cuda_stream
+        stream = self._stream(q_nope.get_device(), stream)
         ev0, ev1 = (None, None) if attn_events is None else attn_events
         L.mla_prefill_run(self.handle, q_nope.data_ptr(), q_rope.data_ptr(), kv_rows.data_ptr(),
                           cu_seqlens.data_ptr(), w_uk.data_ptr(), w_uv.data_ptr(), out.data_ptr(),
                           self.workspace.data_ptr(), self.workspace_bytes, stream, ev0, ev1)
-
-    def read_status(self, stream: Optional[int] = None) -> int:
-        import torch
-        if stream is None:
-            stream = torch.cuda.current_stream(self.workspace.device).cuda_stream
-        return L.mla_decode_read_status(self.workspace.data_ptr(), stream)
 
     def close(self) -> None:
         if self.handle:

@@ -7,7 +7,10 @@ import torch
 
 import mla_latent_kv_21_b200 as M
 
-from harness_paged import block_tables, check_attention, generator, paged_kv
+from mla_workloads import WORKLOADS, generate
+
+from harness import assert_close, dims_of, oracle_out, to_device
+from harness_paged import block_tables, check_attention, f64, generator, paged_kv
 
 pytestmark = pytest.mark.gpu
 
@@ -159,3 +162,93 @@ def test_a_workspace_on_another_device_is_refused(cuda_device):
     plan._at = 1, plan._at[1]
     with pytest.raises(ValueError, match="the workspace is on device 1"):
         c.run(plan, "decode")
+
+
+# ------------------------------------------------------------- the latent plans --
+class Latent:
+    """A latent decode step (bf16 or FP8 cache), or the MLA-form prefill of three prompts."""
+
+    def __init__(self, what, device):
+        self.what, lens = what, [70, 300, 5]
+        self.wl = WORKLOADS["deepseek_v3_fp8" if what == "fp8" else "deepseek_v3"].with_(heads=16)
+        self.inputs = generate(self.wl, seq_lens=lens)
+        self.dev = to_device(self.inputs, device)
+        self.lens = lens
+        if what == "prefill":
+            gen = torch.Generator(device=device).manual_seed(8)
+            T = sum(lens)
+            self.x = [torch.randn(shape, device=device, generator=gen).to(torch.bfloat16)
+                      for shape in ((T, 16, 128), (T, 16, 64), (T, 576))]
+            self.x.append(torch.tensor([0, 70, 370, 375], dtype=torch.int32, device=device))
+        self.shape = (sum(lens), 16, 128) if what == "prefill" else (3, 1, 16, 128)
+        self.device = device
+        # loads the kernels, which may synchronise
+        self.want = self.empty()
+        self.launch(self.make(), self.want)
+        torch.cuda.synchronize()
+        if what != "prefill":
+            assert_close(f64(self.want), oracle_out(self.wl, self.inputs), self.wl.dtype, what)
+
+    def empty(self):
+        return torch.full(self.shape, float("nan"), dtype=torch.bfloat16, device=self.device)
+
+    def make(self):
+        return (M.PrefillPlan if self.what == "prefill" else M.DecodePlan)(dims_of(self.wl), self.lens)
+
+    def launch(self, plan, out, stream=None):
+        d = self.dev
+        if self.what == "prefill":
+            plan.run(*self.x, d["w_uk"], d["w_uv"], out, stream=stream)
+        elif self.what == "fp8":
+            plan.run_fp8(d["q_nope"], d["q_rope"], d["kv_codes"], d["kv_rope"], d["kv_scale"], d["block_table"],
+                         d["seq_lens"], d["w_uk"], d["w_uv"], out, stream=stream)
+        else:
+            plan.run(d["q_nope"], d["q_rope"], d["kv_pool"], d["block_table"], d["seq_lens"], d["w_uk"], d["w_uv"], out,
+                     stream=stream)
+
+
+@pytest.mark.parametrize("what", ["bf16", "fp8", "prefill"])
+def test_latent_plans_on_other_streams(cuda_device, what):
+    """Dropped while the call waits; first used on a stream before the busy one has cleared the workspace."""
+    c = Latent(what, cuda_device)
+    side = torch.cuda.Stream(cuda_device)
+    _keep_busy(side, cuda_device)
+    out = c.empty()
+    torch.cuda.synchronize()
+    busy = _keep_busy(side, cuda_device)
+    plan = c.make()
+    c.launch(plan, out, side.cuda_stream)
+    size, at = plan.workspace_bytes, plan.workspace.data_ptr()
+    del plan
+    assert not side.query()
+    others = [torch.full((size,), 0x5b, dtype=torch.uint8, device=cuda_device) for _ in range(2)]
+    ranges = [(t.data_ptr(), t.data_ptr() + size) for t in others]
+    torch.cuda.synchronize()
+    assert all(at + size <= lo or hi <= at for lo, hi in ranges)
+    assert torch.equal(out, c.want)
+    del busy, others
+    out = c.empty()
+    plan = c.make()
+    torch.cuda.synchronize()
+    busy = _keep_busy(torch.cuda.current_stream(), cuda_device)
+    plan.allocate_workspace(cuda_device)
+    c.launch(plan, out, side.cuda_stream)
+    assert not side.query()
+    torch.cuda.synchronize()
+    assert plan.read_status() == 0 and torch.equal(out, c.want)
+    del busy
+
+
+@pytest.mark.parametrize("what", ["bf16", "prefill"])
+def test_latent_plans_may_run_first_under_a_capture(cuda_device, what):
+    """Their workspace is then the graph's memory, as it always was."""
+    c = Latent(what, cuda_device)
+    plan, out = c.make(), c.empty()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.launch(plan, out)
+    g.replay()
+    torch.cuda.synchronize()
+    assert plan.read_status() == 0 and torch.equal(out, c.want)
+    del g
