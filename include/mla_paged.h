@@ -35,8 +35,9 @@
  * workspace's status word (mla_decode_read_status), while the work it concerns
  * is skipped. Calls run on the current device, which must be the stream's. A
  * workspace belongs to one call in flight at a time (two streams or two graphs
- * that may overlap need one each); it is initialised once with
- * mla_workspace_init.
+ * that may overlap need one each: the results of calls that share one are not
+ * defined, though both end and write nothing but their own outputs); it is
+ * initialised once with mla_workspace_init.
  */
 #ifndef MLA_PAGED_H
 #define MLA_PAGED_H

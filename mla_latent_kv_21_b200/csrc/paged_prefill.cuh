@@ -296,27 +296,34 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       Item x{};
       int64_t ticket = blockIdx.x;
       for (bool more = true; more && ok; ++items) {
-        x.b = -1;
-        if (p.order) {
-          if (ticket < (int64_t)p.order_state[1] * p.Hk) {
-            const int2 at = p.order[ticket / p.Hk];
-            x.b = at.x;
-            x.hk = (int32_t)(ticket % p.Hk);
-            x.t0 = (int64_t)at.y * 2 * tokens;
+        // One lane reads and the warp agrees on what it read. The list lies in the
+        // workspace: where two calls share one by mistake its entries may be another
+        // call's, and none is followed out of this call's sequences.
+        int32_t b = -1, pair = 0;
+        if (lane == 0) {
+          if (p.order) {
+            if (ticket >= 0 && ticket < (int64_t)min(p.order_state[1], p.order_room) * p.Hk) {
+              const int2 at = p.order[ticket / p.Hk];
+              b = at.x;
+              pair = at.y;
+              if (b < 0 || b >= p.B || pair < 0 || (int64_t)pair * 2 * tokens >= new_tokens(p, b, false)) {
+                record_error(p.status, MLA_ERR_BOUNDS);
+                b = -1;
+              }
+            }
+          } else if (items == 0) {       // one item per block
+            b = blockIdx.x % (p.B * p.Hk) / p.Hk;
+            pair = blockIdx.x / (p.B * p.Hk);
+            if ((int64_t)pair * 2 * tokens >= new_tokens(p, b, pair == 0)) b = -1;
           }
-        } else if (items == 0) {         // one item per block
-          const int32_t bh = blockIdx.x % (p.B * p.Hk);
-          x.b = bh / p.Hk;
-          x.hk = bh % p.Hk;
-          x.t0 = (int64_t)(blockIdx.x / (p.B * p.Hk)) * 2 * tokens;
         }
-        if (x.b >= 0) {
-          x.n = new_tokens(p, x.b, lane == 0 && x.t0 == 0);
-          if (x.t0 >= x.n) x.b = -1;
-        }
+        x.b = __shfl_sync(0xffffffffu, b, 0);
+        x.t0 = (int64_t)__shfl_sync(0xffffffffu, pair, 0) * 2 * tokens;
+        x.hk = (int32_t)(p.order ? ticket % p.Hk : blockIdx.x % p.Hk);
         more = x.b >= 0;
         if (more) {
           x.c0 = p.cu[x.b];
+          x.n = new_tokens(p, x.b, false);
           x.L = checked_len(p, x.b, lane == 0);
           x.ahead = x.L - x.n;
           x.two_tiles = x.t0 + tokens < x.n;

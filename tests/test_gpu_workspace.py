@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import mla_latent_kv_21_b200 as M
+from mla_latent_kv_21_b200 import _lib as L
 
 from mla_workloads import WORKLOADS, generate
 
@@ -162,6 +163,64 @@ def test_a_workspace_on_another_device_is_refused(cuda_device):
     plan._at = 1, plan._at[1]
     with pytest.raises(ValueError, match="the workspace is on device 1"):
         c.run(plan, "decode")
+
+
+def _batch(lens, new, Hk, d, device, seed):
+    """Tensors of a decode (new None) or a prefill call and a function that launches it with a workspace."""
+    gen = torch.Generator(device=device).manual_seed(seed)
+    table, blocks = block_tables(lens, generator(seed))
+    kp, vp = (torch.randn((blocks, Hk, 64, d), device=device, generator=gen).to(torch.bfloat16) for _ in range(2))
+    bt, sl = table.to(device), torch.tensor(lens, dtype=torch.int32, device=device)
+    dims = M.gqa_dims_for(4 * Hk, Hk, d, d ** -0.5, "bf16")
+    if new is None:
+        plan, size = L.mla_gqa_decode_plan(dims, lens)
+        q = torch.randn((len(lens), 1, 4 * Hk, d), device=device, generator=gen).to(torch.bfloat16)
+    else:
+        plan, size = L.mla_gqa_prefill_plan(dims, new)
+        q = torch.randn((sum(new), 4 * Hk, d), device=device, generator=gen).to(torch.bfloat16)
+        cu = torch.tensor([sum(new[:b]) for b in range(len(new) + 1)], dtype=torch.int32, device=device)
+
+    def launch(out, workspace, stream):
+        if new is None:
+            L.mla_gqa_decode_run(plan, q.data_ptr(), kp.data_ptr(), vp.data_ptr(), blocks, bt.data_ptr(), bt.shape[1],
+                                 sl.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel(), stream)
+        else:
+            L.mla_gqa_prefill_run(plan, q.data_ptr(), kp.data_ptr(), vp.data_ptr(), blocks, bt.data_ptr(), bt.shape[1],
+                                  cu.data_ptr(), sl.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.numel(),
+                                  stream)
+    return size, torch.zeros_like(q), launch
+
+
+@pytest.mark.parametrize("what", ["decode", "prefill"])
+def test_a_workspace_that_two_calls_share_by_mistake(cuda_device, what):
+    """Against the rule, two calls in flight use one workspace: their results are not defined, but nothing outside of
+    the calls' own tensors is touched, both end, and the next calls in order are right."""
+    if what == "decode":
+        calls = [_batch([1 + 37 * b % 900 for b in range(300)], None, 2, 128, cuda_device, 1),
+                 _batch([0, 40000], None, 1, 128, cuda_device, 2)]
+    else:
+        calls = [_batch([70] * 500, [1 + b % 7 for b in range(500)], 2, 64, cuda_device, 3),
+                 _batch([1500, 900, 2000], [1300, 900, 700], 8, 128, cuda_device, 4)]
+    workspace = torch.zeros(max(c[0] for c in calls), dtype=torch.uint8, device=cuda_device)
+    streams = [torch.cuda.Stream(cuda_device) for _ in calls]
+    current = torch.cuda.current_stream(cuda_device).cuda_stream
+    want = []
+    for _, out, launch in calls:
+        launch(out, workspace, current)
+        torch.cuda.synchronize()
+        want.append(out.clone())
+    assert L.mla_decode_read_status(workspace.data_ptr(), current) == 0
+    for _ in range(30):
+        for (_, out, launch), stream in zip(calls, streams):
+            launch(out, workspace, stream.cuda_stream)
+    torch.cuda.synchronize()
+    assert L.mla_decode_read_status(workspace.data_ptr(), current) in (0, M.MLA_ERR_BOUNDS)
+    for (_, out, launch), ref in zip(calls, want):
+        out.fill_(float("nan"))
+        launch(out, workspace, current)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    assert L.mla_decode_read_status(workspace.data_ptr(), current) == 0
 
 
 # ------------------------------------------------------------- the latent plans --
