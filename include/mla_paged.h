@@ -31,7 +31,7 @@
  * caller owns every device buffer, nothing allocates or synchronises, and what
  * is wrong on the device (a block id outside [0, num_blocks), a length outside
  * [0, 64 block_table_stride] or above 2^31 - 4096, rows of cu_seqlens outside the packed tensors, a
- * position outside the rotation table) is recorded as MLA_ERR_BOUNDS in the
+ * position outside the rotation table, an append of more packed tokens than L_b) is recorded as MLA_ERR_BOUNDS in the
  * workspace's status word (mla_decode_read_status), while the work it concerns
  * is skipped. Calls run on the current device, which must be the stream's. A
  * workspace belongs to one call in flight at a time (two streams or two graphs
@@ -69,11 +69,14 @@ typedef struct {
  * Token t of a sequence b (i = t - cu[b], or t mod Lq without cu_seqlens) has
  * the position L_b - n_b + i, which gives its page, its slot and its row of the
  * rotation table: fp32 [rope_positions, D], cos of the D/2 angles in the first
- * half of the columns, sin in the second (any base or scaling). Rotation in
- * fp32, one rounding to the stored type. Sources may be views: strides count
- * elements, the last dimension is contiguous. An output may be its own source
- * (q_out = q with the same strides as a contiguous [T, H, D]); otherwise
- * outputs and caches may not overlap the sources. */
+ * half of the columns, sin in the second (any base or scaling). Without
+ * cu_seqlens a slot of L_b < Lq tokens (0: an idle slot) has only the last L_b
+ * of its Lq rows, as in the grouped-head decode; its other rows are like rows
+ * that belong to no sequence. Rotation in fp32, one rounding to the stored
+ * type. Sources may be views: strides count elements, the last dimension is
+ * contiguous. An output may be its own source (q_out = q with the same strides
+ * as a contiguous [T, H, D]); otherwise outputs and caches may not overlap the
+ * sources. */
 typedef struct {
   const void* k;                 /* [T, Hk, d] */
   int64_t k_token_stride, k_head_stride;

@@ -39,7 +39,8 @@ namespace pg {
 
 // Where token t goes: its position and its row slot in the cache (block * 64 +
 // slot), or pos = -1 if it has no place (not a token of a sequence, or an
-// error, which is recorded by the calling thread if `tell`).
+// error, which is recorded by the calling thread if `tell`). The lengths are the
+// decode's: without prefix sums those below Lq are none.
 struct Place {
   int64_t pos;
   int64_t block;
@@ -67,7 +68,9 @@ __device__ __forceinline__ Place place_of(const AppendParams& p, const CuSearch&
     i = t - (int64_t)b * p.Lq;
   }
   const int64_t L = p.seq_lens[b], pos = L - n + i;
-  bool ok = L >= n && L <= kMaxLen && L <= (int64_t)p.bt_stride * kPage && (p.D == 0 || pos < p.table_rows);
+  // without prefix sums a slot of L < Lq tokens (0: idle) has only its last L rows
+  if (!p.cu && L >= 0 && pos < 0) return r;
+  bool ok = L >= (p.cu ? n : 0) && L <= kMaxLen && L <= (int64_t)p.bt_stride * kPage && (p.D == 0 || pos < p.table_rows);
   if (ok) {
     r.block = p.block_table[(int64_t)b * p.bt_stride + pos / kPage];
     r.slot = (int32_t)(pos % kPage);

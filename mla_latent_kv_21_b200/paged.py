@@ -94,7 +94,7 @@ class GqaAppend(_Bound):
         """k, v [T, Hk, d] and q [T, Hq, d]: the new tokens before rotation (views whose last dimension is contiguous);
         k_pool, v_pool [num_blocks, Hk, 64, d]; block_table int32 [B, *]; seq_lens int32 [B] with the new tokens counted;
         rope_table float32 [positions, rope_dim]; q_out [T, Hq, d], the rotated queries; cu_seqlens int32 [B + 1], or
-        None: dims.q_len new tokens for every sequence."""
+        None: dims.q_len new tokens for every sequence (where the cache holds fewer, 0 in an idle slot, its last ones)."""
         import torch
         d, act, i32 = self.dims, self._dtype, torch.int32
         Hq, Hk, hd, D, P = self._sizes

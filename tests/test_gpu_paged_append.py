@@ -214,6 +214,30 @@ def test_gqa_graph_and_stream(cuda_device):
     del g
 
 
+IDLE = [70, 0, 1, 2, 64, 0, 200, 3]   # with Lq new tokens each: idle slots, and caches shorter than Lq
+
+
+def _kept(n):
+    """(rows with a place, (new, all) tokens as they are appended) of a step of n tokens over IDLE."""
+    rows = [b * n + i for b, L in enumerate(IDLE) for i in range(n) if i >= n - L]
+    return rows, [(min(n, L), L) for L in IDLE]
+
+
+@pytest.mark.parametrize("n", [1, 3])
+def test_gqa_step_with_idle_and_short_slots(cuda_device, n):
+    """The lengths that the decode takes: a slot without a token is no error, one with L < Lq takes its last L tokens."""
+    c = Gqa([(n, L) for L in IDLE], 8, 2, 128, 128, "bf16", cuda_device, packed=False)
+    c.run()
+    assert c.op.read_status() == 0
+    rows, counts = _kept(n)
+    c.check(rows=rows, counts=counts)
+    others = [t for t in range(n * len(IDLE)) if t not in rows]
+    assert (c.q_out[others] == 9.0).all()
+    c.sl[1] = -1        # a negative length is one
+    c.run()
+    assert c.op.read_status() == M.MLA_ERR_BOUNDS
+
+
 # ---------------------------------------------------------------- latent cache --
 class Latent:
     def __init__(self, counts, H, r, D, dtype, device, seed=2, style="half", packed=True, rows=True, shift=0, positions=256,
@@ -325,6 +349,18 @@ def test_latent_step(cuda_device, dtype, B, n):
     c.run()
     assert c.op.read_status() == 0
     c.check()
+
+
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("dtype,r,D", [("bf16", 512, 64), ("fp32", 512, 64), ("fp8", 512, 64), ("bf16", 50, 6)])
+def test_latent_step_with_idle_and_short_slots(cuda_device, dtype, r, D, n):
+    c = Latent([(n, L) for L in IDLE], 16, r, D, dtype, cuda_device, packed=False)
+    c.run()
+    assert c.op.read_status() == 0
+    rows, counts = _kept(n)
+    c.check(rows=rows, counts=counts)
+    others = [t for t in range(n * len(IDLE)) if t not in rows]
+    assert (c.q_out[others] == 9.0).all() and (c.rows[others] == 9.0).all()
 
 
 @pytest.mark.parametrize("std", [1e-30, 1e-3, 1e4])

@@ -60,6 +60,40 @@ def test_gqa_serving(cuda_device, dtype, Hq, Hk, d):
             at += n
 
 
+@pytest.mark.parametrize("n", [1, 2])
+def test_gqa_steps_with_idle_slots(cuda_device, n):
+    """A served batch of fixed slots: some idle, one shorter than the step, filled and emptied between steps; append and
+    decode take the same lengths, without an error, and a query without a key gives zeros."""
+    Hq, Hk, d, B = 16, 4, 128, 6
+    gen = generator(25)
+    table, blocks = block_tables([200] * B, gen)
+    bt = table.to(cuda_device)
+    kp, vp = (torch.randn((blocks, Hk, 64, d), generator=gen).to(torch.bfloat16).to(cuda_device) for _ in range(2))
+    rope = M.rope_table(200, d, device=cuda_device)
+    dims = M.gqa_dims_for(Hq, Hk, d, d ** -0.5, "bf16", q_len=n, rope_dim=d)
+    append = M.GqaAppend(dims).allocate_workspace(cuda_device)
+    decode = M.GqaDecodePlan(dims, [100] * B).allocate_workspace(cuda_device)
+    done = []
+    for lens in ([0, 1, 130, 0, 64, 65], [n, 0, 130 + n, 0, 0, 65 + n], [0] * B):
+        qkv = torch.randn((B * n, Hq + 2 * Hk, d), generator=gen).to(torch.bfloat16).to(cuda_device)
+        sl = torch.tensor(lens, dtype=torch.int32, device=cuda_device)
+        q = torch.full((B * n, Hq, d), float("nan"), dtype=torch.bfloat16, device=cuda_device)
+        out = q.clone()
+        append.run(qkv[:, Hq:Hq + Hk], qkv[:, Hq + Hk:], kp, vp, bt, sl, rope, q=qkv[:, :Hq], q_out=q)
+        decode.run(q.view(B, n, Hq, d), kp, vp, bt, sl, out.view(B, n, Hq, d))
+        done.append((lens, q, out.view(B, n, Hq, d), kp.clone(), vp.clone()))
+    assert append.read_status() == 0 and decode.read_status() == 0
+    for lens, q, out, k_now, v_now in done:
+        for b, L in enumerate(lens):
+            seen = min(n, L)       # the queries with a key
+            assert (out[b, :n - seen] == 0).all() and torch.isnan(q.view(B, n, Hq, d)[b, :n - seen]).all()
+            if seen:
+                pages = table[b, :-(-L // 64)].long()
+                k, v = (p.cpu()[pages].transpose(1, 2).reshape(-1, Hk, d)[:L] for p in (k_now, v_now))
+                check_attention(out[b, n - seen:], q.view(B, n, Hq, d)[b, n - seen:], k, v, d ** -0.5, torch.bfloat16,
+                                f"slot {b} of {lens}")
+
+
 def _latent_inputs(T, H, gen, device):
     kv = torch.randn((T, 576), generator=gen).to(torch.bfloat16).to(device)
     q = torch.randn((T, H, 192), generator=gen).to(torch.bfloat16).to(device)
