@@ -13,7 +13,7 @@ using namespace mla;
 
 struct mla_gqa_decode_plan {
   mla_gqa_dims_t dims;
-  int32_t B, W;
+  int32_t B, W, key_parts;
   size_t o_off, ml_off, tails_off, total;
 };
 
@@ -67,6 +67,23 @@ mla_status_t launched(cudaError_t e) {
 // append of 16K tokens 118 / 107 us.
 int heads_per_block(int64_t token_blocks, int H, int lanes) {
   return lanes * (token_blocks * ((H + 16 * lanes - 1) / (16 * lanes)) >= 1184 ? 16 : 4);
+}
+
+// How the four warps of a decode worker share a page where up to 16 rows read it:
+// four key parts, or two key parts times two halves of the output columns. The
+// halves compute the scores twice and join a quarter as much when a segment ends.
+// At d = 128 they suit short segments; at d = 64 very short and long ones, for a
+// reason that is not established. By the mean pages of a segment (a sequence's share of one worker); four key parts
+// against halves, graph replay, medians of seven runs in turn, us:
+//   d = 128: 0.9 pages (256 x 64, 8 heads) 29.0 / 24.5, 3.1 (128 x 200) 33.0 / 31.2, 5 (64 x
+//     500) 30.3 / 29.9, 12 (1 x 60000, 4 heads) 31.4 / 31.1, 15 (32 x 2000) 51.0 / 51.0,
+//     20 (16 x 2048, 32 heads) 90.6 / 91.1, 27 (1 x 131071, 4 heads) 53.3 / 53.3,
+//     30 (16 x 3000) 128.1 / 128.9, 41 (16 x 4096) 170.7 / 173.3, 81 (16 x 8192) 328.8 / 332.8
+//   d = 64: 0.9 pages 21.8 / 19.7, 1.7 (1 x 4000) 9.7 / 9.6, 3.1 23.1 / 23.4, 10 (16 x 1000, 32
+//     heads) 29.6 / 30.8, 12 22.2 / 22.7, 15 30.1 / 30.4, 22 (32 x 3000) 40.0 / 39.8, 30 71.0 / 67.5,
+//     41 92.9 / 90.4, 81 176.7 / 168.0
+bool four_key_parts(int d, int64_t pages, int64_t segments) {
+  return d == 128 ? pages >= 16 * segments : pages >= 3 * segments && pages < 20 * segments;
 }
 
 // Rows of the cache and of the batch: tensor-map and grid coordinates are 32-bit.
@@ -236,6 +253,7 @@ mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, cons
   p->dims = d;
   p->B = batch;
   p->W = (int32_t)std::max<int64_t>(1, std::min<int64_t>({most, pages, 4096}));
+  p->key_parts = four_key_parts(d.head_dim, pages, p->W + items);
   const size_t rows = (size_t)2 * p->W * G * d.q_len;
   p->o_off = kHeaderBytes;
   p->ml_off = align_up(p->o_off + rows * d.head_dim * sizeof(float), 1024);
@@ -278,6 +296,7 @@ mla_status_t mla_gqa_decode_run(mla_gqa_decode_plan_t plan, const void* q, const
   p.Hk = d.num_kv_heads;
   p.G = p.Hq / p.Hk;
   p.W = plan->W;
+  p.key_parts = plan->key_parts;
   p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   const int64_t items = (int64_t)p.B * p.Hk;

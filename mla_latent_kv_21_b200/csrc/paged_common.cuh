@@ -43,6 +43,7 @@ struct GqaParams {
   int2* tails;             // per worker, the item it began and did not finish
   int64_t num_blocks, T;
   int32_t bt_stride, B, Lq, Hq, Hk, G, W;
+  int32_t key_parts;       // decode, up to 16 rows: four key parts, no column halves
   int32_t max_new;         // prefill: largest count of the plan
   int2* order;             // prefill workspace: (sequence, pair of tiles), longest first; NULL: one item per block
   int32_t* order_state;    // workspace header: {items drawn, items}

@@ -20,13 +20,10 @@
 // hold, and the fragments stay in registers from the scores to the weighted
 // sum. MT = 1, 2 or 4 tiles of 16 rows. With 2 tiles two warps share a tile and
 // take half the keys of each page, with their own running maximum and sum, joined
-// when the segment ends; with 1 tile there are two such pairs, each with half of
-// the output columns (both compute the same scores, 16 more products a page, and
-// the join moves a quarter of what four key parts would). Against four key parts, three
-// runs of each in turn: 256 x 64 tokens 26.2 us instead of 30.3, 1 x 500 7.65 instead
-// of 8.2, 128 x 200 31.1 instead of 32.7, but 16 x 8192 334.4 instead of 330.1 and 32 x
-// 2000 50.9 instead of 50.6: the scores that are computed twice show where the memory
-// is the bound. Four column parts: 363 at 16 x 8192.
+// when the segment ends. With 1 tile there are two layouts (key_parts): four such
+// warps, or two pairs, each with half of the output columns (both compute the same
+// scores, 16 more products a page, and the join moves a quarter of what four key
+// parts would).
 //
 // Measured on one B200 (graph replay): 16 x 8192 tokens, 32 heads of their own,
 // 2147.7 MB in 331 to 338 us (6.4 to 6.5 TB/s; the copy rate is 6.55); 1 x 131071
@@ -140,13 +137,13 @@ struct Segments {
   }
 };
 
-template <typename T, int kD, int MT>
+// kHalves: warps with the same rows and keys, each with its output columns
+template <typename T, int kD, int MT, int kHalves>
 __global__ void __launch_bounds__(kDecodeThreads, 2)
     gqa_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, GqaParams p) {
   using namespace ptx;
   using S = DecodeSmem<kD>;
   using WS = WeightScale<T>;
-  constexpr int kHalves = MT == 1 ? 2 : 1;         // warps with the same rows and keys, each with its output columns
   constexpr int kParts = 4 / (MT * kHalves);       // warps with the same rows and columns, each with its keys
   constexpr int kKeys = kPage / kParts;            // keys of a page per warp
   constexpr int NT = kKeys / 8;
@@ -600,12 +597,12 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(GqaParams p, int
 }
 
 // ------------------------------------------------------------------ host ---
-template <typename T, int kD, int MT>
+template <typename T, int kD, int MT, int kHalves>
 cudaError_t launch_decode_tiles(const GqaParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, cudaStream_t stream) {
   using S = DecodeSmem<kD>;
-  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(gqa_decode_kernel<T, kD, MT>), (int)S::alloc);
+  cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(gqa_decode_kernel<T, kD, MT, kHalves>), (int)S::alloc);
   if (e != cudaSuccess) return e;
-  return launch_dependent(gqa_decode_kernel<T, kD, MT>, dim3(p.W), dim3(kDecodeThreads), S::alloc, stream, tm_k, tm_v, p);
+  return launch_dependent(gqa_decode_kernel<T, kD, MT, kHalves>, dim3(p.W), dim3(kDecodeThreads), S::alloc, stream, tm_k, tm_v, p);
 }
 
 template <typename T, int kD>
@@ -615,9 +612,10 @@ cudaError_t launch_decode(const GqaParams& p, int64_t items, cudaStream_t stream
   if (!pool_map(&tm_k, p.k_pool, p.num_blocks * p.Hk, kD, bf16) || !pool_map(&tm_v, p.v_pool, p.num_blocks * p.Hk, kD, bf16))
     return cudaErrorInvalidValue;
   const int rows = p.G * p.Lq;
-  cudaError_t e = rows <= 16 ? launch_decode_tiles<T, kD, 1>(p, tm_k, tm_v, stream)
-                : rows <= 32 ? launch_decode_tiles<T, kD, 2>(p, tm_k, tm_v, stream)
-                             : launch_decode_tiles<T, kD, 4>(p, tm_k, tm_v, stream);
+  cudaError_t e = rows > 32   ? launch_decode_tiles<T, kD, 4, 1>(p, tm_k, tm_v, stream)
+                : rows > 16   ? launch_decode_tiles<T, kD, 2, 1>(p, tm_k, tm_v, stream)
+                : p.key_parts ? launch_decode_tiles<T, kD, 1, 1>(p, tm_k, tm_v, stream)
+                              : launch_decode_tiles<T, kD, 1, 2>(p, tm_k, tm_v, stream);
   if (e != cudaSuccess || p.W == 1) return e;
   // Where workers outnumber items, about every W / items-th begins one, of about
   // as many parts. A block looks through that many workers; the more parts, the

@@ -110,6 +110,22 @@ def test_plan_lengths_affect_balance_only(cuda_device):
         _check(out, q, seqs, 128, "bf16", f"planned {planned}")
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp16", 64)])
+@pytest.mark.parametrize("Hk,G,Lq", [(2, 4, 1), (1, 16, 1), (2, 5, 3)])
+def test_both_layouts_of_the_warps(cuda_device, dtype, d, Hk, G, Lq):
+    """Plans for short, medium and long segments choose how the warps share a page; each with the same ragged lengths."""
+    lens = [1, 63, 64, 65, 0, 700, 2000, 5]
+    dev, q, seqs = _inputs(lens, Hk, G, d, Lq, TYPES[dtype], 17, cuda_device)
+    for planned, workers in ((64, 0), (64 * 8, 1), (64 * 10, 3), (64 * 200, 5), (64 * 200, 300)):
+        plan = M.GqaDecodePlan(_dims(Hk, G, d, Lq, dtype), [planned] * len(lens), num_workers=workers)
+        plan.allocate_workspace(cuda_device)
+        out = torch.full_like(dev["q"], float("nan"))
+        _run(plan, dev, out)
+        assert plan.read_status() == 0
+        _check(out, q, seqs, d, dtype, f"planned {planned}, {workers} workers")
+        plan.close()
+
+
 def test_bad_lengths_and_blocks_are_recorded(cuda_device):
     """A length past the table or below zero counts as 0; a page whose block is out of range is not seen; the other
     sequences are right."""
