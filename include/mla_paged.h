@@ -164,6 +164,18 @@ mla_status_t mla_gqa_decode_run(mla_gqa_decode_plan_t plan, const void* q, const
 
 void mla_gqa_decode_plan_destroy(mla_gqa_decode_plan_t plan);
 
+/* Self-test of the timeout path (diagnostics, as mla_decode_selftest_timeout): a
+ * run whose ring slots are never given back, with every wait bounded by
+ * wait_limit_ns (1000 to 2e9). Where a worker has more pages than its ring holds
+ * (3 at d = 128, 6 at d = 64) the waits run out: the kernel returns,
+ * MLA_ERR_DEVICE_TIMEOUT is recorded and `out` is not defined. The plan and the
+ * workspace stay usable. */
+mla_status_t mla_gqa_decode_selftest_timeout(mla_gqa_decode_plan_t plan, const void* q, const void* k_pool,
+                                             const void* v_pool, int64_t num_blocks, const int32_t* block_table,
+                                             int32_t block_table_stride, const int32_t* seq_lens_dev, void* out,
+                                             void* workspace, size_t workspace_bytes, uint64_t wait_limit_ns,
+                                             void* stream);
+
 /* ---- Prefill over the grouped-head cache -----------------------------------
  * Causal attention of the n_b new tokens of each sequence over all its L_b
  * tokens, whose keys and values are in the cache already (appended before this
@@ -184,6 +196,14 @@ mla_status_t mla_gqa_prefill_run(mla_gqa_prefill_plan_t plan, const void* q, con
                                  void* workspace, size_t workspace_bytes, void* stream);
 
 void mla_gqa_prefill_plan_destroy(mla_gqa_prefill_plan_t plan);
+
+/* Self-test of the timeout path: as mla_gqa_decode_selftest_timeout, with the
+ * softmax weights of a step never handed over to the second product. */
+mla_status_t mla_gqa_prefill_selftest_timeout(mla_gqa_prefill_plan_t plan, const void* q, const void* k_pool,
+                                              const void* v_pool, int64_t num_blocks, const int32_t* block_table,
+                                              int32_t block_table_stride, const int32_t* cu_seqlens_dev,
+                                              const int32_t* seq_lens_dev, void* out, void* workspace,
+                                              size_t workspace_bytes, uint64_t wait_limit_ns, void* stream);
 
 #ifdef __cplusplus
 }

@@ -55,6 +55,7 @@ EXPORTED = (
     "mla_gqa_append", "mla_latent_append",
     "mla_gqa_decode_plan", "mla_gqa_decode_run", "mla_gqa_decode_plan_destroy",
     "mla_gqa_prefill_plan", "mla_gqa_prefill_run", "mla_gqa_prefill_plan_destroy",
+    "mla_gqa_decode_selftest_timeout", "mla_gqa_prefill_selftest_timeout",
 )
 
 
@@ -160,6 +161,9 @@ _lib.mla_gqa_decode_plan.argtypes = [ctypes.POINTER(mla_gqa_dims_t), _i32, _i32p
                                      ctypes.POINTER(_vp), ctypes.POINTER(_sz)]
 _lib.mla_gqa_decode_run.restype = ctypes.c_int
 _lib.mla_gqa_decode_run.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _sz, _vp]
+_lib.mla_gqa_decode_selftest_timeout.restype = ctypes.c_int
+_lib.mla_gqa_decode_selftest_timeout.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _sz,
+                                                 ctypes.c_uint64, _vp]
 _lib.mla_gqa_decode_plan_destroy.restype = None
 _lib.mla_gqa_decode_plan_destroy.argtypes = [_vp]
 _lib.mla_gqa_prefill_plan.restype = ctypes.c_int
@@ -167,6 +171,9 @@ _lib.mla_gqa_prefill_plan.argtypes = [ctypes.POINTER(mla_gqa_dims_t), _i32, _i32
                                       ctypes.POINTER(_sz)]
 _lib.mla_gqa_prefill_run.restype = ctypes.c_int
 _lib.mla_gqa_prefill_run.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _sz, _vp]
+_lib.mla_gqa_prefill_selftest_timeout.restype = ctypes.c_int
+_lib.mla_gqa_prefill_selftest_timeout.argtypes = [_vp, _vp, _vp, _vp, _i64, _vp, _i32, _vp, _vp, _vp, _vp, _sz,
+                                                  ctypes.c_uint64, _vp]
 _lib.mla_gqa_prefill_plan_destroy.restype = None
 _lib.mla_gqa_prefill_plan_destroy.argtypes = [_vp]
 _lib.mla_workspace_init.restype = ctypes.c_int
@@ -344,6 +351,14 @@ def mla_gqa_decode_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_t
                                    seq_lens_dev, out, workspace, workspace_bytes, stream), "mla_gqa_decode_run")
 
 
+def mla_gqa_decode_selftest_timeout(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride, seq_lens_dev,
+                                    out, workspace, workspace_bytes, wait_limit_ns, stream=0) -> None:
+    """Diagnostics: a run whose waits run out (see the C header)."""
+    _check(_lib.mla_gqa_decode_selftest_timeout(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride,
+                                                seq_lens_dev, out, workspace, workspace_bytes, wait_limit_ns, stream),
+           "mla_gqa_decode_selftest_timeout")
+
+
 def mla_gqa_decode_plan_destroy(plan) -> None:
     _lib.mla_gqa_decode_plan_destroy(plan)
 
@@ -361,6 +376,15 @@ def mla_gqa_prefill_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_
     _check(_lib.mla_gqa_prefill_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride,
                                     cu_seqlens_dev, seq_lens_dev, out, workspace, workspace_bytes, stream),
            "mla_gqa_prefill_run")
+
+
+def mla_gqa_prefill_selftest_timeout(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride,
+                                     cu_seqlens_dev, seq_lens_dev, out, workspace, workspace_bytes, wait_limit_ns,
+                                     stream=0) -> None:
+    """Diagnostics: a run whose waits run out (see the C header)."""
+    _check(_lib.mla_gqa_prefill_selftest_timeout(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride,
+                                                 cu_seqlens_dev, seq_lens_dev, out, workspace, workspace_bytes,
+                                                 wait_limit_ns, stream), "mla_gqa_prefill_selftest_timeout")
 
 
 def mla_gqa_prefill_plan_destroy(plan) -> None:

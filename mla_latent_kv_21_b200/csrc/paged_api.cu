@@ -89,6 +89,106 @@ bool four_key_parts(int d, int64_t pages, int64_t segments) {
 // Rows of the cache and of the batch: tensor-map and grid coordinates are 32-bit.
 bool fits32(int64_t rows) { return rows < (int64_t(1) << 31); }
 
+// The waits of one run: the normal limit, or a self-test of the timeout path
+// (short limit, barriers that expect one arrival more than they get).
+struct Waits {
+  uint64_t limit_ns = ptx::kWaitLimitNs;
+  int32_t withhold = 0;
+};
+
+bool selftest_limit(uint64_t ns) { return ns >= 1000 && ns <= ptx::kWaitLimitNs; }
+
+mla_status_t decode_run(mla_gqa_decode_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
+                        int64_t num_blocks, const int32_t* block_table, int32_t block_table_stride,
+                        const int32_t* seq_lens_dev, void* out, void* workspace, size_t workspace_bytes, void* stream_,
+                        Waits waits) {
+  if (!plan || !q || !k_pool || !v_pool || !block_table || !seq_lens_dev || !out || !workspace || num_blocks < 1 ||
+      block_table_stride < 1 || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < plan->total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const mla_gqa_dims_t& d = plan->dims;
+  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  char* ws = static_cast<char*>(workspace);
+  GqaParams p{};
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.out = out;
+  p.status = reinterpret_cast<int32_t*>(ws);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens_dev;
+  p.o_part = reinterpret_cast<float*>(ws + plan->o_off);
+  p.ml_part = reinterpret_cast<float2*>(ws + plan->ml_off);
+  p.tails = reinterpret_cast<int2*>(ws + plan->tails_off);
+  p.wait_limit_ns = waits.limit_ns;
+  p.withhold = waits.withhold;
+  p.num_blocks = num_blocks;
+  p.bt_stride = block_table_stride;
+  p.B = plan->B;
+  p.Lq = d.q_len;
+  p.T = (int64_t)plan->B * d.q_len;
+  p.Hq = d.num_q_heads;
+  p.Hk = d.num_kv_heads;
+  p.G = p.Hq / p.Hk;
+  p.W = plan->W;
+  p.key_parts = plan->key_parts;
+  p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const int64_t items = (int64_t)p.B * p.Hk;
+  const bool bf = d.dtype == MLA_BF16;
+  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_decode<__nv_bfloat16, 128>(p, items, stream)
+                      : bf                      ? pg::launch_decode<__nv_bfloat16, 64>(p, items, stream)
+                      : d.head_dim == 128       ? pg::launch_decode<__half, 128>(p, items, stream)
+                                                : pg::launch_decode<__half, 64>(p, items, stream);
+  return launched(e);
+}
+
+mla_status_t prefill_run(mla_gqa_prefill_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
+                         int64_t num_blocks, const int32_t* block_table, int32_t block_table_stride,
+                         const int32_t* cu_seqlens_dev, const int32_t* seq_lens_dev, void* out, void* workspace,
+                         size_t workspace_bytes, void* stream_, Waits waits) {
+  if (!plan || !workspace || num_blocks < 1 || block_table_stride < 1) return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < plan->total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (plan->T == 0) return MLA_OK;
+  if (!q || !k_pool || !v_pool || !block_table || !cu_seqlens_dev || !seq_lens_dev || !out || !aligned16(q) ||
+      !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
+    return MLA_ERR_INVALID_ARG;
+  const mla_gqa_dims_t& d = plan->dims;
+  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  GqaParams p{};
+  p.q = q;
+  p.k_pool = k_pool;
+  p.v_pool = v_pool;
+  p.out = out;
+  p.status = static_cast<int32_t*>(workspace);
+  p.block_table = block_table;
+  p.seq_lens = seq_lens_dev;
+  p.cu = cu_seqlens_dev;
+  p.num_blocks = num_blocks;
+  p.bt_stride = block_table_stride;
+  p.B = plan->B;
+  p.T = plan->T;
+  p.Hq = d.num_q_heads;
+  p.Hk = d.num_kv_heads;
+  p.G = p.Hq / p.Hk;
+  p.max_new = plan->max_new;
+  p.order_state = static_cast<int32_t*>(workspace) + 4;
+  p.order = reinterpret_cast<int2*>(static_cast<char*>(workspace) + kHeaderBytes);
+  p.order_room = plan->order_room;
+  int32_t sms = 0;
+  if (!sm_count(&sms)) return MLA_ERR_NO_DEVICE;
+  p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
+  p.wait_limit_ns = waits.limit_ns;
+  p.withhold = waits.withhold;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
+  const bool bf = d.dtype == MLA_BF16;
+  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_prefill<__nv_bfloat16, 128>(p, sms, stream)
+                      : bf                      ? pg::launch_prefill<__nv_bfloat16, 64>(p, sms, stream)
+                      : d.head_dim == 128       ? pg::launch_prefill<__half, 128>(p, sms, stream)
+                                                : pg::launch_prefill<__half, 64>(p, sms, stream);
+  return launched(e);
+}
+
 }  // namespace
 
 extern "C" {
@@ -267,45 +367,19 @@ mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, cons
 mla_status_t mla_gqa_decode_run(mla_gqa_decode_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
                                 int64_t num_blocks, const int32_t* block_table, int32_t block_table_stride,
                                 const int32_t* seq_lens_dev, void* out, void* workspace, size_t workspace_bytes,
-                                void* stream_) {
-  if (!plan || !q || !k_pool || !v_pool || !block_table || !seq_lens_dev || !out || !workspace || num_blocks < 1 ||
-      block_table_stride < 1 || !aligned16(q) || !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
-    return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes < plan->total) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  const mla_gqa_dims_t& d = plan->dims;
-  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
-  char* ws = static_cast<char*>(workspace);
-  GqaParams p{};
-  p.q = q;
-  p.k_pool = k_pool;
-  p.v_pool = v_pool;
-  p.out = out;
-  p.status = reinterpret_cast<int32_t*>(ws);
-  p.block_table = block_table;
-  p.seq_lens = seq_lens_dev;
-  p.o_part = reinterpret_cast<float*>(ws + plan->o_off);
-  p.ml_part = reinterpret_cast<float2*>(ws + plan->ml_off);
-  p.tails = reinterpret_cast<int2*>(ws + plan->tails_off);
-  p.wait_limit_ns = ptx::kWaitLimitNs;
-  p.num_blocks = num_blocks;
-  p.bt_stride = block_table_stride;
-  p.B = plan->B;
-  p.Lq = d.q_len;
-  p.T = (int64_t)plan->B * d.q_len;
-  p.Hq = d.num_q_heads;
-  p.Hk = d.num_kv_heads;
-  p.G = p.Hq / p.Hk;
-  p.W = plan->W;
-  p.key_parts = plan->key_parts;
-  p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const int64_t items = (int64_t)p.B * p.Hk;
-  const bool bf = d.dtype == MLA_BF16;
-  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_decode<__nv_bfloat16, 128>(p, items, stream)
-                      : bf                      ? pg::launch_decode<__nv_bfloat16, 64>(p, items, stream)
-                      : d.head_dim == 128       ? pg::launch_decode<__half, 128>(p, items, stream)
-                                                : pg::launch_decode<__half, 64>(p, items, stream);
-  return launched(e);
+                                void* stream) {
+  return decode_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride, seq_lens_dev, out, workspace,
+                    workspace_bytes, stream, Waits{});
+}
+
+mla_status_t mla_gqa_decode_selftest_timeout(mla_gqa_decode_plan_t plan, const void* q, const void* k_pool,
+                                             const void* v_pool, int64_t num_blocks, const int32_t* block_table,
+                                             int32_t block_table_stride, const int32_t* seq_lens_dev, void* out,
+                                             void* workspace, size_t workspace_bytes, uint64_t wait_limit_ns,
+                                             void* stream) {
+  if (!selftest_limit(wait_limit_ns)) return MLA_ERR_INVALID_ARG;
+  return decode_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride, seq_lens_dev, out, workspace,
+                    workspace_bytes, stream, Waits{wait_limit_ns, 1});
 }
 
 void mla_gqa_decode_plan_destroy(mla_gqa_decode_plan_t plan) { delete plan; }
@@ -343,46 +417,19 @@ mla_status_t mla_gqa_prefill_plan(const mla_gqa_dims_t* dims, int32_t batch, con
 mla_status_t mla_gqa_prefill_run(mla_gqa_prefill_plan_t plan, const void* q, const void* k_pool, const void* v_pool,
                                  int64_t num_blocks, const int32_t* block_table, int32_t block_table_stride,
                                  const int32_t* cu_seqlens_dev, const int32_t* seq_lens_dev, void* out,
-                                 void* workspace, size_t workspace_bytes, void* stream_) {
-  if (!plan || !workspace || num_blocks < 1 || block_table_stride < 1) return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes < plan->total) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  if (plan->T == 0) return MLA_OK;
-  if (!q || !k_pool || !v_pool || !block_table || !cu_seqlens_dev || !seq_lens_dev || !out || !aligned16(q) ||
-      !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
-    return MLA_ERR_INVALID_ARG;
-  const mla_gqa_dims_t& d = plan->dims;
-  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
-  GqaParams p{};
-  p.q = q;
-  p.k_pool = k_pool;
-  p.v_pool = v_pool;
-  p.out = out;
-  p.status = static_cast<int32_t*>(workspace);
-  p.block_table = block_table;
-  p.seq_lens = seq_lens_dev;
-  p.cu = cu_seqlens_dev;
-  p.num_blocks = num_blocks;
-  p.bt_stride = block_table_stride;
-  p.B = plan->B;
-  p.T = plan->T;
-  p.Hq = d.num_q_heads;
-  p.Hk = d.num_kv_heads;
-  p.G = p.Hq / p.Hk;
-  p.max_new = plan->max_new;
-  p.order_state = static_cast<int32_t*>(workspace) + 4;
-  p.order = reinterpret_cast<int2*>(static_cast<char*>(workspace) + kHeaderBytes);
-  p.order_room = plan->order_room;
-  int32_t sms = 0;
-  if (!sm_count(&sms)) return MLA_ERR_NO_DEVICE;
-  p.scale_log2 = d.softmax_scale * 1.4426950408889634f;
-  p.wait_limit_ns = ptx::kWaitLimitNs;
-  cudaStream_t stream = static_cast<cudaStream_t>(stream_);
-  const bool bf = d.dtype == MLA_BF16;
-  const cudaError_t e = bf && d.head_dim == 128 ? pg::launch_prefill<__nv_bfloat16, 128>(p, sms, stream)
-                      : bf                      ? pg::launch_prefill<__nv_bfloat16, 64>(p, sms, stream)
-                      : d.head_dim == 128       ? pg::launch_prefill<__half, 128>(p, sms, stream)
-                                                : pg::launch_prefill<__half, 64>(p, sms, stream);
-  return launched(e);
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  return prefill_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride, cu_seqlens_dev, seq_lens_dev,
+                     out, workspace, workspace_bytes, stream, Waits{});
+}
+
+mla_status_t mla_gqa_prefill_selftest_timeout(mla_gqa_prefill_plan_t plan, const void* q, const void* k_pool,
+                                              const void* v_pool, int64_t num_blocks, const int32_t* block_table,
+                                              int32_t block_table_stride, const int32_t* cu_seqlens_dev,
+                                              const int32_t* seq_lens_dev, void* out, void* workspace,
+                                              size_t workspace_bytes, uint64_t wait_limit_ns, void* stream) {
+  if (!selftest_limit(wait_limit_ns)) return MLA_ERR_INVALID_ARG;
+  return prefill_run(plan, q, k_pool, v_pool, num_blocks, block_table, block_table_stride, cu_seqlens_dev, seq_lens_dev,
+                     out, workspace, workspace_bytes, stream, Waits{wait_limit_ns, 1});
 }
 
 void mla_gqa_prefill_plan_destroy(mla_gqa_prefill_plan_t plan) { delete plan; }

@@ -50,6 +50,7 @@ struct GqaParams {
   int32_t order_room;
   float scale_log2;
   uint64_t wait_limit_ns;
+  int32_t withhold;        // self-test of the timeout path only: barriers that one arrival too few completes
 };
 
 namespace pg {

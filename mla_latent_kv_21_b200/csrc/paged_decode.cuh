@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(kDecodeThreads, 2)
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::slots; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 4);
+      mbar_init(empty(s), 4 + p.withhold);
     }
     fence_mbarrier_init_cluster();
     prefetch_tmap(&tm_k);

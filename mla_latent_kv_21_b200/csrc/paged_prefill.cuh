@@ -229,16 +229,17 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
   auto o_full = [&](int i) -> uint32_t { return bar(2 * kSlots + 10 + i); };
   auto o_empty = [&](int i) -> uint32_t { return bar(2 * kSlots + 12 + i); };
   const uint32_t w_full = bar(2 * kSlots + 14), w_empty = bar(2 * kSlots + 15);   // the work item
+  const uint32_t drained = bar(2 * kSlots + 16);                                  // after a timeout
   Item* work = reinterpret_cast<Item*>(gbase + S::work);
-  static_assert(sizeof(Item) <= 128 && 8 * (2 * kSlots + 16) <= 320, "shared memory layout");
+  static_assert(sizeof(Item) <= 128 && 8 * (2 * kSlots + 17) <= 320, "shared memory layout");
   uint32_t* tslot = reinterpret_cast<uint32_t*>(gbase + S::misc);
   const int tokens = kTile / p.G, used = tokens * p.G;              // of one tile
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < 2 * kSlots + 16; ++i) mbar_init(bar(i), 1);
+    for (int i = 0; i < 2 * kSlots + 17; ++i) mbar_init(bar(i), 1);
     for (int i = 0; i < 2; ++i) {        // the four softmax warps of the tile
       mbar_init(p_part(i), 4);
-      mbar_init(p_full(i), 4);
+      mbar_init(p_full(i), 4 + p.withhold);
       mbar_init(o_empty(i), 4);
     }
     mbar_init(w_empty, 10);              // producer, MMA issuer, softmax warps
@@ -499,7 +500,14 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       }
       // the last commit has arrived before the block ends
       if (it > 0) wait(empty((it - 1) % kSlots), ((it - 1) / kSlots) & 1);
-      if (!ok && lane == 0) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
+      if (!ok) {
+        if (lane == 0) record_error(p.status, MLA_ERR_DEVICE_TIMEOUT);
+        // products that were issued are complete before their operands and
+        // accumulators are given back
+        if (leader) tc_commit<1>(drained);
+        __syncwarp();
+        (void)mbar_wait(drained, 0, p.wait_limit_ns);
+      }
       __syncwarp();
     }
   } else {

@@ -92,6 +92,25 @@ def test_null_and_misaligned_pointers():
     L.mla_gqa_prefill_plan_destroy(plan)
 
 
+def test_timeout_selftest_limits():
+    """[1 us, 2 s], checked before any device work."""
+    fake = 1 << 20
+    plan, ws = L.mla_gqa_decode_plan(_dims(), [100], num_sms=148)
+    plan2, ws2 = L.mla_gqa_prefill_plan(_dims(), [100])
+    for limit in (0, 999, 2_000_000_001):
+        with pytest.raises(M.MlaError) as e:
+            L.mla_gqa_decode_selftest_timeout(plan, fake, fake, fake, 4, fake, 2, fake, fake, fake, ws, limit)
+        assert e.value.status == L.MLA_ERR_INVALID_ARG
+        with pytest.raises(M.MlaError) as e:
+            L.mla_gqa_prefill_selftest_timeout(plan2, fake, fake, fake, 4, fake, 2, fake, fake, fake, fake, ws2, limit)
+        assert e.value.status == L.MLA_ERR_INVALID_ARG
+    with pytest.raises(M.MlaError) as e:
+        L.mla_gqa_decode_selftest_timeout(plan, fake, fake, fake, 4, fake, 2, fake, fake, fake, ws - 1, 1_000_000)
+    assert e.value.status == L.MLA_ERR_WORKSPACE_TOO_SMALL
+    L.mla_gqa_decode_plan_destroy(plan)
+    L.mla_gqa_prefill_plan_destroy(plan2)
+
+
 def _gqa_args(**kw):
     f = 1 << 20
     a = dict(k=f, k_token_stride=256, k_head_stride=128, v=f, v_token_stride=256, v_head_stride=128, q=f, q_token_stride=1024,
