@@ -88,6 +88,7 @@ bool four_key_parts(int d, int64_t pages, int64_t segments) {
 
 // Rows of the cache and of the batch: tensor-map and grid coordinates are 32-bit.
 bool fits32(int64_t rows) { return rows < (int64_t(1) << 31); }
+bool fits32(int64_t blocks, int32_t heads) { return fits32(blocks) && fits32(blocks * heads); }
 
 // The waits of one run: the normal limit, or a self-test of the timeout path
 // (short limit, barriers that expect one arrival more than they get).
@@ -107,7 +108,7 @@ mla_status_t decode_run(mla_gqa_decode_plan_t plan, const void* q, const void* k
     return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < plan->total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const mla_gqa_dims_t& d = plan->dims;
-  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  if (!fits32(num_blocks, d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
   char* ws = static_cast<char*>(workspace);
   GqaParams p{};
   p.q = q;
@@ -154,7 +155,7 @@ mla_status_t prefill_run(mla_gqa_prefill_plan_t plan, const void* q, const void*
       !aligned16(k_pool) || !aligned16(v_pool) || !aligned16(out))
     return MLA_ERR_INVALID_ARG;
   const mla_gqa_dims_t& d = plan->dims;
-  if (!fits32(num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  if (!fits32(num_blocks, d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
   GqaParams p{};
   p.q = q;
   p.k_pool = k_pool;
@@ -212,7 +213,7 @@ mla_status_t mla_gqa_append(const mla_gqa_dims_t* dims, const mla_gqa_append_arg
       !aligned16(a.v_pool) || !aligned16(a.rope_table) || !multiple(a.k_token_stride, a.k_head_stride, 8) ||
       !multiple(a.v_token_stride, a.v_head_stride, 8) || (a.q && !multiple(a.q_token_stride, a.q_head_stride, 8)))
     return MLA_ERR_INVALID_ARG;
-  if (!fits32(a.num_tokens) || !fits32(a.num_blocks * d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
+  if (!fits32(a.num_tokens) || !fits32(a.num_blocks, d.num_kv_heads)) return MLA_ERR_UNSUPPORTED;
   AppendParams p{};
   p.k = a.k; p.k_ts = a.k_token_stride; p.k_hs = a.k_head_stride;
   p.v = a.v; p.v_ts = a.v_token_stride; p.v_hs = a.v_head_stride;

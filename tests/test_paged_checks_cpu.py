@@ -92,6 +92,22 @@ def test_null_and_misaligned_pointers():
     L.mla_gqa_prefill_plan_destroy(plan)
 
 
+def test_block_counts_whose_product_overflows():
+    """num_blocks times the key heads past 64 bits is too many, not few."""
+    fake = 1 << 20
+    plan, ws = L.mla_gqa_decode_plan(_dims(), [100], num_sms=148)
+    plan2, ws2 = L.mla_gqa_prefill_plan(_dims(), [100])
+    for blocks in (2 ** 62, 2 ** 63 - 1):
+        for call in (lambda: L.mla_gqa_decode_run(plan, fake, fake, fake, blocks, fake, 2, fake, fake, fake, ws),
+                     lambda: L.mla_gqa_prefill_run(plan2, fake, fake, fake, blocks, fake, 2, fake, fake, fake, fake, ws2),
+                     lambda: L.mla_gqa_append(_dims(), _gqa_args(num_blocks=blocks), fake, 1024)):
+            with pytest.raises(M.MlaError) as e:
+                call()
+            assert e.value.status == L.MLA_ERR_UNSUPPORTED
+    L.mla_gqa_decode_plan_destroy(plan)
+    L.mla_gqa_prefill_plan_destroy(plan2)
+
+
 def test_timeout_selftest_limits():
     """[1 us, 2 s], checked before any device work."""
     fake = 1 << 20
