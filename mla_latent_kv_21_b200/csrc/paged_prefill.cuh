@@ -295,37 +295,43 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
     if (warp == 2) {
       // ---------------------------------------------------------- scheduler --
       Item x{};
-      int64_t ticket = blockIdx.x;
+      uint32_t ticket = blockIdx.x;
       for (bool more = true; more && ok; ++items) {
         // One lane reads and the warp agrees on what it read. The list lies in the
         // workspace: where two calls share one by mistake its entries may be another
         // call's, and none is followed out of this call's sequences.
-        int32_t b = -1, pair = 0;
+        int32_t b = -1, pair = 0, c0 = 0, n = 0, L = 0;
         if (lane == 0) {
+          const uint32_t place = ticket / (uint32_t)p.Hk;
           if (p.order) {
-            if (ticket >= 0 && ticket < (int64_t)min(p.order_state[1], p.order_room) * p.Hk) {
-              const int2 at = p.order[ticket / p.Hk];
+            const int32_t count = min(p.order_state[1], p.order_room);
+            const int2 at = p.order[min(place, (uint32_t)p.order_room - 1)];   // read beside the count
+            if (count > 0 && place < (uint32_t)count) {
               b = at.x;
               pair = at.y;
-              if (b < 0 || b >= p.B || pair < 0 || (int64_t)pair * 2 * tokens >= new_tokens(p, b, false)) {
-                record_error(p.status, MLA_ERR_BOUNDS);
-                b = -1;
-              }
+              if (b < 0 || b >= p.B || pair < 0) b = -2;
             }
           } else if (items == 0) {       // one item per block
-            b = blockIdx.x % (p.B * p.Hk) / p.Hk;
-            pair = blockIdx.x / (p.B * p.Hk);
-            if ((int64_t)pair * 2 * tokens >= new_tokens(p, b, pair == 0)) b = -1;
+            b = (int32_t)(place % (uint32_t)p.B);
+            pair = (int32_t)(place / (uint32_t)p.B);
           }
+          if (b >= 0) {
+            c0 = p.cu[b];
+            L = checked_len(p, b, false);
+            n = (int32_t)new_tokens(p, b, !p.order && pair == 0);
+            if ((int64_t)pair * 2 * tokens >= n) b = p.order ? -2 : -1;
+            else if (L == 0) (void)checked_len(p, b, true);
+          }
+          if (b == -2) record_error(p.status, MLA_ERR_BOUNDS);
         }
         x.b = __shfl_sync(0xffffffffu, b, 0);
-        x.t0 = (int64_t)__shfl_sync(0xffffffffu, pair, 0) * 2 * tokens;
-        x.hk = (int32_t)(p.order ? ticket % p.Hk : blockIdx.x % p.Hk);
         more = x.b >= 0;
         if (more) {
-          x.c0 = p.cu[x.b];
-          x.n = new_tokens(p, x.b, false);
-          x.L = checked_len(p, x.b, lane == 0);
+          x.hk = (int32_t)(ticket % (uint32_t)p.Hk);
+          x.t0 = (int64_t)__shfl_sync(0xffffffffu, pair, 0) * 2 * tokens;
+          x.c0 = __shfl_sync(0xffffffffu, c0, 0);
+          x.n = __shfl_sync(0xffffffffu, n, 0);
+          x.L = __shfl_sync(0xffffffffu, L, 0);
           x.ahead = x.L - x.n;
           x.two_tiles = x.t0 + tokens < x.n;
           x.nk0 = steps_to(x.ahead, min(x.t0 + tokens, x.n));
@@ -347,7 +353,7 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
         if (lane == 0) {
           *work = x;
           mbar_arrive_local(w_full);
-          if (more && p.order) ticket = (int64_t)gridDim.x + atomicAdd(p.order_state, 1);
+          if (more && p.order) ticket = gridDim.x + (uint32_t)atomicAdd(p.order_state, 1);
         }
         ticket = __shfl_sync(0xffffffffu, ticket, 0);
       }
