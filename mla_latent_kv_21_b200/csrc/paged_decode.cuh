@@ -523,7 +523,6 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(GqaParams p, int
   constexpr int E = kD / 32;                 // kAhead: parts whose loads are in flight
   __shared__ float so[8][kD];
   __shared__ float sm[8], sl[8];
-  __shared__ int2 begun[32];
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -531,20 +530,15 @@ __global__ void __launch_bounds__(kJoinThreads) gqa_join_kernel(GqaParams p, int
   const int row = blockIdx.y * per + warp / share, first = warp % share;
   const int w_end = min(p.W - 1, (int)(blockIdx.x + 1) * group);
   for (int w0 = blockIdx.x * group; w0 < w_end; w0 += 32) {
-    // One warp reads what the workers left and the block agrees on it. It lies in
-    // the workspace: where two calls share one by mistake it may be another call's,
-    // and none is followed out of this call's items and workers.
-    if (w0 != blockIdx.x * group) __syncthreads();   // the last ones have been read
-    if (warp == 0) {
-      int2 t = w0 + lane < w_end ? p.tails[w0 + lane] : make_int2(-1, 0);
-      if (t.x >= 0 && (t.x >= p.B * p.Hk || t.y < w0 + lane || t.y >= p.W)) {
-        record_error(p.status, MLA_ERR_BOUNDS);
-        t.x = -1;
-      }
-      begun[lane] = t;
+    // What the workers left lies in the workspace: where two calls share one by
+    // mistake it may be another call's, and none is followed out of this call's
+    // items and workers. (Warps that then see different items leave at different
+    // times; a barrier waits for those that are left.)
+    int2 mine = w0 + lane < w_end ? p.tails[w0 + lane] : make_int2(-1, 0);
+    if (mine.x >= p.B * p.Hk || mine.y >= p.W) {
+      record_error(p.status, MLA_ERR_BOUNDS);
+      mine.x = -1;
     }
-    __syncthreads();
-    const int2 mine = begun[lane];
     uint32_t open = __ballot_sync(0xffffffffu, mine.x >= 0);
     for (; open; open &= open - 1) {          // the same for every warp
       const int i0 = __ffs(open) - 1, w = w0 + i0;
