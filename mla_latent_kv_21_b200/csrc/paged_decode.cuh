@@ -612,17 +612,24 @@ cudaError_t launch_decode(const GqaParams& p, int64_t items, cudaStream_t stream
                               : launch_decode_tiles<T, kD, 1, 2>(p, tm_k, tm_v, stream);
   if (e != cudaSuccess || p.W == 1) return e;
   // Where workers outnumber items, about every W / items-th begins one, of about
-  // as many parts. A block looks through that many workers; the more parts, the
-  // more warps to a row and loads in flight. (One block per worker and four
-  // loads throughout took 18.6 us instead of 14.3 at 8 x 4000 tokens, one key
-  // head, 32 rows; batches of whole items do not change.) Joining in the decode
-  // kernel, by the worker that comes last, was slower: 9.3 us against 8.3 at
-  // 1 x 500, 35 against 30 at 64 x 500.
-  const int group = (int)std::max<int64_t>(1, p.W / items);
-  const int per = group <= 4 ? 8 : group <= 24 ? 2 : 1;
+  // as many parts. A block looks through that many workers; a row has one, four or
+  // eight warps, and a warp as many loads in flight as it has parts, up to 8.
+  // Measured at 22 shapes with 1, 2, 4 and 8 warps to a row and 4 or 8 loads; the
+  // borders' sides, us: 5 parts (8 x 2000, 8 key heads, 32 rows) one warp with 4 / 8
+  // loads 23.0 / 21.6, four warps 24.8 / 29.3; 8 parts (1 x 500, 8 key heads) one warp
+  // 7.6 / 7.3, four 7.6 / 7.8; 10 parts (4 x 8000, 8 key heads) one warp 30.1 / 29.8, four
+  // 29.5 / 29.2, with 32 rows 34.8 / 33.4 and 32.5 / 34.7; 25 parts (3 x 9000, 4 key heads, 16
+  // rows) four 19.3 / 18.0, eight 18.3 / 17.9; 37 parts (8 x 4000, one key head, 32 rows)
+  // four 14.5 / 13.5, eight 13.1 / 12.4; 100 parts (1 x 20000, one key head) four 14.3 / 14.1,
+  // eight 12.6 / 12.3. (From 70 parts on, blocks that look through a quarter of the
+  // workers would gain up to 8%: 1 x 100000, one key head, 25.4 / 23.3.) Joining in the
+  // decode kernel, by the worker that comes last, was slower: 9.3 us against 8.3 at
+  // 1 x 500, 35 against 30 at 64 x 500 (with the first form of this kernel).
+  const int group = (int)std::max<int64_t>(1, p.W / items), parts = (int)ceil_div64(p.W, items);
+  const int per = parts <= 8 ? 8 : parts <= 32 ? 2 : 1;
   const dim3 grid((unsigned)((p.W - 1 + group - 1) / group), (unsigned)((rows + per - 1) / per));
-  return group <= 24 ? launch_dependent(gqa_join_kernel<T, kD, 4>, grid, dim3(kJoinThreads), 0, stream, p, group, per)
-                     : launch_dependent(gqa_join_kernel<T, kD, 8>, grid, dim3(kJoinThreads), 0, stream, p, group, per);
+  return parts * per <= 4 * 8 ? launch_dependent(gqa_join_kernel<T, kD, 4>, grid, dim3(kJoinThreads), 0, stream, p, group, per)
+                              : launch_dependent(gqa_join_kernel<T, kD, 8>, grid, dim3(kJoinThreads), 0, stream, p, group, per);
 }
 
 }  // namespace pg
