@@ -61,7 +61,9 @@ typedef struct {
   int32_t page_size;      /* tokens per cache block; 64 */
   int32_t rope_dim;       /* D: leading elements of a head that append rotates; 0 (none) or a multiple of 16 up to d */
   int32_t rope_style;     /* mla_rope_style_t */
-  int32_t dtype;          /* MLA_BF16 or MLA_FP16: activations, caches and outputs */
+  int32_t dtype;          /* MLA_BF16 or MLA_FP16: activations, caches and outputs. Attention rounds the softmax
+                             weights to it once, before the product with the values; scores, maxima, sums and
+                             accumulators are fp32 */
   float softmax_scale;    /* multiplies q.k; usually 1/sqrt(d) */
 } mla_gqa_dims_t;
 

@@ -62,7 +62,7 @@ mla_status_t launched(cudaError_t e) {
 
 // Heads of a block of an append whose threads stand for `lanes` heads: 16 per
 // thread where that still fills the machine (its angles are then loaded once for
-// them; 1184 blocks are 8 to an SM), else 4 (one batch of loads). Measured with 4 / 8 / 16 / 32: grouped-head
+// them; 1184 blocks are 8 to each of a B200's 148 SMs), else 4 (one batch of loads). Measured with 4 / 8 / 16 / 32: grouped-head
 // append of 14K tokens 60.2 / 55.0 / 51.8 / 50.2 us; with 8 / 16 in the latent
 // append of 16K tokens 118 / 107 us.
 int heads_per_block(int64_t token_blocks, int H, int lanes) {
@@ -346,8 +346,8 @@ mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, cons
   // Two workers per SM, down to one page each; only an item cut into more than
   // about 100 parts of a few pages costs more to join than it gains. Measured
   // with one key head, 20000 tokens (313 pages) and 8 / 16 / 64 rows: 296 workers
-  // 17.7 / 17.9 / 22.1 us, 104 workers 12.4 / 13.0 / 18.9, 52 workers 12.5 / 13.0
-  // / 24.3; with 8 key heads, 500 tokens: 64 workers 8.2, 32 8.1, 16 9.9.
+  // 17.3 / 17.4 / 21.3 us, 104 workers 11.6 / 11.7 / 18.0, 52 workers 12.5 / 12.6
+  // / 21.6; with 8 key heads, 500 tokens: 64 workers 7.4, 32 7.8, 16 9.7.
   const int64_t most = o.num_workers > 0 ? o.num_workers : std::min<int64_t>(2 * sms, std::max(100 * items, pages / 4));
   struct mla_gqa_decode_plan* p = new (std::nothrow) struct mla_gqa_decode_plan();
   if (!p) return MLA_ERR_INVALID_ARG;

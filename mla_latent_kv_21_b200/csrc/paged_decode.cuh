@@ -26,11 +26,13 @@
 // parts would).
 //
 // Measured on one B200 (graph replay): 16 x 8192 tokens, 32 heads of their own,
-// 2147.7 MB in 331 to 338 us (6.4 to 6.5 TB/s; the copy rate is 6.55); 1 x 131071
-// tokens, 64 / 4 heads, 53 us (5.0 TB/s); 64 x 500, 32 / 8 heads, 30 us (4.4 TB/s); one page 4.3 us. A
-// segment's fixed part (queries, joining the warps, storing, the latency of one
-// page) is thousands of cycles, most of it instruction fetch: loading the next
-// segment's queries early changed no case by more than 2%.
+// 2147.7 MB in 328 to 331 us (6.5 TB/s; the copy rate is 6.55); 1 x 131071 tokens,
+// 64 / 4 heads, 53 to 55 us (4.9 to 5.1 TB/s); 64 x 500, 32 / 8 heads, 30 us (4.4 TB/s);
+// one page 3.9 us. A segment's fixed part (queries, joining the warps, storing, the
+// latency of one page) is thousands of cycles. At 256 x 64 tokens a warp that does
+// not issue waits for loads (2.3 warps per issued instruction) or for fixed
+// latencies (2.1), less for shared memory (0.7), barriers (0.6) and instructions
+// (0.4); loading the next segment's queries early changed no case by more than 2%.
 #pragma once
 
 #include "paged_common.cuh"
@@ -40,7 +42,8 @@ namespace pg {
 
 constexpr int kDecodeThreads = 160;
 // Loading an item's queries, joining the warps and storing takes a worker about
-// as long as this many pages. Measured (graph replay, two runs of each in turn) at 64
+// as long as this many pages. Measured (graph replay, two runs of each in turn, with
+// column halves where there are up to 16 rows) at 64
 // sequences of 1 to 16384 tokens, 8 key heads (many items of one page): 90.5 us with
 // 0, 56.7 with 2, 56.6 with 3, 56.1 with 4, 56.8 with 6; at 128 x 200 tokens 31.5, 30.6,
 // 30.9, 31.1 and 31.3, at 32 x 4000 with 32 rows a key head 97.9, 97.2, 96.8, 97.4 and

@@ -32,8 +32,8 @@
 // chain of one tile is scores in tensor memory -> registers 70, maximum 370,
 // weights 1450 (1024 of special-function unit, shared with the other tile's
 // warps), P V and Q K^T 1180; the tensor core is busy for 2048 of the cycles at
-// d = 128. At 8K tokens that is 427 us from cold (1290 TFLOP/s); in a loop the
-// power cap lowers the clock to 1.67 GHz and it takes 480 to 525 us. Tried and
+// d = 128. At 8K tokens that is 437 us while the clock stays at 1965 MHz (1260
+// TFLOP/s); in a loop the power cap lowers it and it takes 480 to 525 us. Tried and
 // no faster: the maximum found beside the first weights, with those made again
 // where it moves (3370 cycles); for d = 64, weights in columns of their own, so
 // that S(j + 1) is computed during the softmax of step j (3700 cycles: the two
@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(kPrefillThreads, 1)
       // --------------------------------------------------------- MMA issuer --
       // The warp stays converged and one elected lane issues: descriptors and
       // addresses are then uniform, and an MMA costs a few issue slots. (Issued
-      // by lane 0 of a diverged warp, the 32 MMAs of a step took 4270 cycles;
-      // a step takes 3350 now.)
+      // by lane 0 of a diverged warp, the 32 MMAs of a step took 4270 cycles; a
+      // step took 3350 with this change, and takes 3190 now.)
       constexpr uint32_t idesc_s = idesc16<T>(128, 128, 0, 0), idesc_o = idesc16<T>(128, kD, 0, 1);
       constexpr std::integral_constant<int, 0> k0{};
       constexpr std::integral_constant<int, kEarlyKeys / 16> kEarly{};
