@@ -486,9 +486,12 @@ mla_status_t mla_decode_read_status(const void* workspace, void* stream_, int32_
   if (!workspace || !device_status) return MLA_ERR_INVALID_ARG;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_);
   int32_t v = 0;
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return MLA_ERR_CUDA;
-  if (cudaMemcpy(&v, workspace, sizeof(v), cudaMemcpyDeviceToHost) != cudaSuccess) return MLA_ERR_CUDA;
-  if (cudaMemset(const_cast<void*>(workspace), 0, sizeof(v)) != cudaSuccess) return MLA_ERR_CUDA;
+  // on the stream, and complete when the call returns: a clearing on the default
+  // stream could come after what the next run on `stream` records
+  if (cudaMemcpyAsync(&v, workspace, sizeof(v), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaMemsetAsync(const_cast<void*>(workspace), 0, sizeof(v), stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return MLA_ERR_CUDA;
   *device_status = v;
   return MLA_OK;
 }

@@ -165,6 +165,29 @@ def test_a_workspace_on_another_device_is_refused(cuda_device):
         c.run(plan, "decode")
 
 
+def test_a_status_is_read_and_cleared_in_the_streams_order(cuda_device):
+    """On a stream of its own, while the default stream is busy: the clearing waits for neither, and an error that the
+    next call records is not cleared with the last one's."""
+    c = Case(cuda_device)
+    side = torch.cuda.Stream(cuda_device)
+    plan = c.make("decode").allocate_workspace(cuda_device)
+    out = c.run(plan, "decode", stream=side.cuda_stream)
+    bad = c.sl.clone()
+    bad[1] = -1
+    torch.cuda.synchronize()
+    default = torch.cuda.default_stream(cuda_device)
+    busy = _keep_busy(default, cuda_device)
+    good, c.sl = c.sl, bad
+    for _ in range(3):
+        c.launch(plan, "decode", out, side.cuda_stream)
+        assert plan.read_status(side.cuda_stream) == M.MLA_ERR_BOUNDS
+    assert not default.query()
+    torch.cuda.synchronize()
+    assert plan.read_status(side.cuda_stream) == 0
+    c.sl = good
+    del busy
+
+
 def _batch(lens, new, Hk, d, device, seed):
     """Tensors of a decode (new None) or a prefill call and a function that launches it with a workspace."""
     gen = torch.Generator(device=device).manual_seed(seed)
