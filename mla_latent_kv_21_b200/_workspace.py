@@ -67,8 +67,9 @@ class Workspace:
         allocated if there is none yet."""
         import torch
         if self.workspace is None:
-            capturing = torch.cuda.is_current_stream_capturing() or (
-                stream is not None and _capturing(stream_of(stream, dev)))
+            with torch.cuda.device(dev):
+                capturing = torch.cuda.is_current_stream_capturing() or (
+                    stream is not None and _capturing(stream_of(stream, dev)))
             if capturing and not self._allocates_under_capture:
                 raise RuntimeError("allocate_workspace() before capturing: memory allocated under a capture belongs "
                                    "to the graph")
