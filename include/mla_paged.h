@@ -154,7 +154,8 @@ typedef struct mla_gqa_decode_plan* mla_gqa_decode_plan_t;
 
 /* seq_lens_host gives the lengths that the plan balances for and chooses the
  * kernel's layout by; the device lengths of a run may differ (results then
- * agree within rounding with those of a plan for them). opts (may be NULL): num_sms and num_workers. */
+ * agree within rounding with those of a plan for them). opts (may be NULL):
+ * num_sms and num_workers. */
 mla_status_t mla_gqa_decode_plan(const mla_gqa_dims_t* dims, int32_t batch, const int32_t* seq_lens_host,
                                  const mla_plan_options_t* opts, mla_gqa_decode_plan_t* plan_out,
                                  size_t* workspace_bytes);

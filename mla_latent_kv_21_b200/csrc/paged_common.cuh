@@ -86,6 +86,12 @@ __device__ __forceinline__ int32_t sequence_of(const CuSearch& s, const int32_t*
   return a < s.B ? a : -1;
 }
 
+// Softmax weights are rounded once, to the 16-bit type: the tensor core takes both
+// operands of the second product in it, and a second term for the residual would
+// double that product. Their sum is of the unrounded weights, in fp32, so an output
+// is off by at most half a step times sum_j p_j |v_j| from that (with random keys
+// 2.2e-3 of the output's norm in bf16 and 2.5e-4 in fp16, where rounding the output
+// alone gives 1.7e-3 and 2.1e-4). ex2.approx adds 2^-22.
 // fp16 softmax weights: 2^-14 is the smallest normal value, so the weights of the
 // largest score are 2^8 instead of 1 and the maximum moves after 2^6; weights
 // then stay below 2^14 and are normal numbers down to 2^-22 of the largest.
