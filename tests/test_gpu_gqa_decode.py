@@ -126,6 +126,35 @@ def test_both_layouts_of_the_warps(cuda_device, dtype, d, Hk, G, Lq):
         plan.close()
 
 
+def test_many_sequences(cuda_device):
+    """More sequences than a worker has threads, many of them idle."""
+    lens = [(b * 37) % 150 if b % 3 else 0 for b in range(2500)]
+    dev, q, seqs = _inputs(lens, 1, 2, 64, 1, torch.float16, 18, cuda_device)
+    for workers in (0, 2):
+        plan = M.GqaDecodePlan(_dims(1, 2, 64, 1, "fp16"), lens, num_workers=workers).allocate_workspace(cuda_device)
+        out = torch.full_like(dev["q"], float("nan"))
+        _run(plan, dev, out)
+        assert plan.read_status() == 0
+        host = out.cpu()
+        for b, (k, v) in enumerate(seqs):
+            check_attention(host[b], q[b], k, v, 64 ** -0.5, torch.float16, f"{workers} workers, sequence {b}")
+        plan.close()
+
+
+@pytest.mark.parametrize("Hk,G,Lq", [(1, 4, 1), (2, 16, 2)])
+def test_as_many_workers_as_pages(cuda_device, Hk, G, Lq):
+    """An item of many parts: the join looks through more workers than a warp has lanes."""
+    lens = [40000, 100]
+    dev, q, seqs = _inputs(lens, Hk, G, 128, Lq, torch.bfloat16, 19, cuda_device)
+    for workers in (4096, 500, 70):
+        plan = M.GqaDecodePlan(_dims(Hk, G, 128, Lq, "bf16"), lens, num_workers=workers).allocate_workspace(cuda_device)
+        out = torch.full_like(dev["q"], float("nan"))
+        _run(plan, dev, out)
+        assert plan.read_status() == 0
+        _check(out, q, seqs, 128, "bf16", f"{workers} workers")
+        plan.close()
+
+
 def test_bad_lengths_and_blocks_are_recorded(cuda_device):
     """A length past the table or below zero counts as 0; a page whose block is out of range is not seen; the other
     sequences are right."""
