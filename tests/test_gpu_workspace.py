@@ -57,11 +57,11 @@ class Case:
 
 
 def _keep_busy(stream, device):
-    """Products of about a tenth of a second on `stream`, with tensors that stay alive."""
+    """Products of a few tenths of a second on `stream`, with tensors that stay alive."""
     with torch.cuda.stream(stream):
         a = torch.randn((8192, 8192), device=device, dtype=torch.bfloat16)
         b = torch.empty_like(a)
-        for _ in range(150):
+        for _ in range(500):
             torch.matmul(a, a, out=b)
     return a, b
 
